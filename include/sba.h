@@ -38,8 +38,8 @@
  *   - Errors: argument checks run on the host before any launch and return an
  *     sba_status without touching device memory.  A failed launch returns
  *     SBA_ERR_CUDA.  Faults detected inside a kernel (a wait that gave up, a
- *     routing entry outside [0, nB_b)) set a device-side error word that
- *     sba_get_device_status reports.
+ *     routing entry outside [0, nB_b), an index outside its table) set a device-side
+ *     error word that sba_get_device_status reports.
  */
 #ifndef SBA_H_
 #define SBA_H_
@@ -58,7 +58,7 @@ typedef enum {
     SBA_ERR_ALIGNMENT = 3,     /* a device pointer not 16-byte aligned */
     SBA_ERR_CUDA = 4,          /* a CUDA runtime or driver call failed */
     SBA_ERR_TIMEOUT = 5,       /* a kernel wait gave up (reported by sba_get_device_status) */
-    SBA_ERR_DEVICE_FLAG = 6,   /* a kernel found a bad routing entry (sba_get_device_status) */
+    SBA_ERR_DEVICE_FLAG = 6,   /* a kernel found a bad routing entry or index (sba_get_device_status) */
     SBA_ERR_SCRATCH_TOO_SMALL = 7  /* problem too large for sba_pool_select_noalloc's fixed scratch */
 } sba_status;
 
@@ -338,6 +338,121 @@ sba_status sba_token_prune_select(const void* x, int B, int N, int C, const int3
 sba_status sba_gather_tokens(const void* src, int B, int H, int N, int row_bytes, const int32_t* idx,
                              const int32_t* valid_len_out, int Npad_out, void* dst, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * The transformer block around the attention: its norms with their gate and residual,
+ * its projections in 8-bit integers, and rotary positions by themselves.  The page
+ * "MiniMax-H3 on 8xH200 benchmark" (news.paixiangai.cn), the kernel layer, names an
+ * indexed AdaLN, a gated residual and QK RMSNorm + 3D RoPE among its fused kernels; the page
+ * "Sol Video Inference Engine" (sjmshsh.github.io) names low-precision projections.
+ * Neither gives formulas: those below are the usual ones.
+ *
+ * These calls take bf16, fp16 or fp32 values (sba_dtype), any sizes, and rows at any
+ * strides whose last dimension is contiguous; strides are in elements, not negative, and
+ * 0 only where an input is broadcast.  Pointers need the alignment of their element only
+ * (16 bytes for int8 codes); rows whose addresses are all multiples of 16 bytes run
+ * faster.  An output may be the input of the same shape, type and strides named below as
+ * allowed; otherwise outputs overlap nothing.  Statistics, sums and products are in fp32
+ * (the integer sums exact) and each output is rounded once, to nearest even.  An index
+ * outside its table raises SBA_ERR_DEVICE_FLAG and reads row 0. */
+typedef enum { SBA_DTYPE_BF16 = 0, SBA_DTYPE_FP16 = 1, SBA_DTYPE_FP32 = 2 } sba_dtype;
+
+#define SBA_NORM_NONE 0
+#define SBA_NORM_LAYER 1 /* (r - mean r) / sqrt(mean (r - mean r)^2 + eps) */
+#define SBA_NORM_RMS 2   /* r / sqrt(mean r^2 + eps) */
+
+/* Widest row of the calls below. */
+#define SBA_MAX_CHANNELS 32768
+
+/* The step between two sub-blocks of a transformer block, in one pass: the gated residual
+ * of the block's output, with an optional norm of that output (a norm after the block),
+ * and the norm of the new residual row with its modulation (the norm before the next).
+ * Per row (b, n) of C channels, with g = index[b][n], or b without an index:
+ *   z = y, or post_norm(y) * post_weight
+ *   r = x + gate[g] * z                                (without y: r = x)
+ *   h = (norm(r) * weight + bias) * (1 + scale[g]) + shift[g]
+ * and, with out_scale given, h in 8 bits: out_scale = max|h| / 127 and
+ * code = nearest integer (ties to even) to fp32(h * fp32(127 / max|h|)); a row with
+ * max|h| < 2^-100 gets codes and scale 0.
+ *   x            [B, N, C] of x_dtype: the residual stream
+ *   y            [B, N, C] of dtype, or NULL
+ *   x_out        [B, N, C] of x_dtype (written): r.  Required with y, unused without;
+ *                may be x
+ *   out          [B, N, C] of dtype (written): h.  May be y (or x, of the same dtype and
+ *                strides).  Unused with norm SBA_NORM_NONE.  With out_scale: int8 codes,
+ *                rows of C rounded up to a multiple of 16 (the last ones 0), 16-byte
+ *                aligned, strides multiples of 16
+ *   out_scale    fp32 [B, N] contiguous (written), or NULL
+ *   x_dtype, dtype  equal, or x_dtype fp32 with a 16-bit dtype
+ *   strides      8 values: (sample, token) strides of x, y, x_out, out
+ *   valid_len    int32 [B] device, or NULL; rows n >= valid_len[b] are not read, and are
+ *                written as 0 (x_out, out, out_scale)
+ *   weight, bias, post_weight  [C] or NULL;  gate, scale, shift  [G, C] contiguous or
+ *                NULL; all of param_dtype, fp32 or dtype
+ *   index        int32 [B, N] contiguous, or NULL (then G >= B)
+ * norm SBA_NORM_NONE is the gated residual alone.  A parameter given without the step that
+ * uses it is SBA_ERR_INVALID_ARG.  HBM-bound: x and y are read once, r and h written once. */
+sba_status sba_residual_norm(const void* x, const void* y, void* x_out, void* out, float* out_scale, int x_dtype,
+                             int dtype, int B, int N, int C, const int64_t* strides, const int32_t* valid_len,
+                             int norm, const void* weight, const void* bias, int post_norm, const void* post_weight,
+                             const void* gate, const void* scale, const void* shift, int param_dtype, int G,
+                             const int32_t* index, float eps, void* stream);
+
+/* Rows in 8 bits with one scale a row, as in sba_residual_norm: the activations' side of
+ * sba_int8_linear, and, row by row, the weights' side.
+ *   x        element (b, h, n, d) at b, h, n strides[0..2] + d, of dtype: [B, H, N, D], the
+ *            attention's head layout; H = 1 for plain rows [B, N, D]
+ *   codes    int8 [B, N, K'] contiguous, 16-byte aligned (written), K' = H * D rounded up
+ *            to a multiple of 16: code h * D + d of row (b, n); the last ones 0
+ *   scales   fp32 [B, N] (written) */
+sba_status sba_token_quantize(const void* x, int dtype, int B, int H, int N, int D, const int64_t* strides,
+                              int8_t* codes, float* scales, void* stream);
+
+#define SBA_ACT_NONE 0
+#define SBA_ACT_GELU_TANH 1
+#define SBA_ACT_SILU 2
+
+/* Largest number of codes whose integer sum fits 32 bits whatever the codes. */
+#define SBA_MAX_INT8_K 131056
+
+/* A projection in 8-bit integers, on the tensor cores, with its epilogue fused:
+ *   acc = sum_k a[b][n][k] * w[m][k]                   (32-bit integers, exact)
+ *   v = act(acc * (a_scale[b][n] * w_scale[m]) + bias[m])
+ *   out[b][n][m] = residual[b][n][m] + gate[g][m] * v,  g = index[b][n], or b
+ *   a, a_scale   int8 [B, N, K] and fp32 [B, N] contiguous, as sba_token_quantize or
+ *                sba_residual_norm write them;  w, w_scale: int8 [M, K] and fp32 [M]
+ *                (sba_token_quantize of the weight's rows).  K a multiple of 16, at most
+ *                SBA_MAX_INT8_K (else SBA_ERR_UNSUPPORTED)
+ *   bias         [M] or NULL;  gate [G, M] contiguous or NULL; of param_dtype, fp32 or
+ *                out_dtype;  index int32 [B, N] contiguous, or NULL (then G >= B)
+ *   activation   SBA_ACT_*;  the tanh form of GELU
+ *   residual     [B, N, M] of out_dtype, or NULL; may be out
+ *   out          (written) of out_dtype.  heads = 0: rows [B, N, M].  heads > 0: the
+ *                attention's layout [B, heads, N, M / heads], M / heads a multiple of 32
+ *   strides      5 values: residual (sample, token); out (sample, head, token) */
+sba_status sba_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale, int B, int N,
+                           int K, int M, const void* bias, const void* gate, int param_dtype, int G,
+                           const int32_t* index, int activation, const void* residual, void* out, int out_dtype,
+                           int heads, const int64_t* strides, void* stream);
+
+#define SBA_ROPE_INTERLEAVED 0 /* pair p = channels (2p, 2p + 1) */
+#define SBA_ROPE_HALF 1        /* pair p = channels (p, p + rope_dim / 2) */
+
+/* Rotary positions: pair p = (u, v) of token n turns by theta = pos[b][n][axis[p]] *
+ * inv_freq[p],
+ *   (u, v) -> amplitude * (u cos theta - v sin theta, u sin theta + v cos theta)
+ * (inverse != 0: by -theta, which is also the gradient).  Channels [rope_dim, D) are copied.
+ * Angles are taken modulo a turn in 64-bit integers, so any int32 position is as exact as
+ * a small one; fp32 arithmetic, one rounding.
+ *   x, out       [B, H, N, D] of dtype at strides (sample, head, token) x, then out;
+ *                out may be x (same strides)
+ *   pos          int32 [B, N, axes] device contiguous
+ *   rope_dim     even, in [2, min(D, 256)]
+ *   inv_freq, axis  host arrays of rope_dim / 2: radians a position, and the position's
+ *                axis, of each pair */
+sba_status sba_rotary(const void* x, void* out, int dtype, const int32_t* pos, int axes, int B, int H, int N, int D,
+                      const int64_t* strides, int rope_dim, int layout, const double* inv_freq, const uint8_t* axis,
+                      float amplitude, int inverse, void* stream);
+
 /* Dense attention over all valid tokens of each sample (the sparsity = 0 case
  * without a routing), same layouts as sba_attention.  On the page "MiniMax-H3 on
  * 8xH200 benchmark", section "How SubBlock sparse attention works", sparsity is the
@@ -352,7 +467,7 @@ sba_status sba_dense_attention(const void* q, const void* k, const void* v, void
  * SBA_ERR_CUDA if the synchronisation itself failed). */
 sba_status sba_get_device_status(void* stream);
 
-/* Limit, in GPU clock cycles, of every wait inside the attention kernel
+/* Limit, in GPU clock cycles, of every wait inside the attention and product kernels
  * (default about 2^32 cycles, i.e. seconds).  A wait that reaches it gives up,
  * sets SBA_ERR_TIMEOUT and lets the kernel exit cleanly.  0 restores the
  * default.  Meant for tests of the timeout path. */

@@ -1,0 +1,173 @@
+// rotary.cuh -- rotary positions of attention inputs: adjacent ("interleaved") or split
+// ("half") channel pairs, on the first rope_dim channels of each head, several position
+// axes, any frequency per pair.
+//
+// The producer (producer.cuh) turns normed Q and K by the 3D rotation of the page
+// "MiniMax-H3 on 8xH200 benchmark" (news.paixiangai.cn); this is the rotation by itself,
+// for models that pair their channels or scale their frequencies otherwise.  Pair p =
+// (u, v) of a token at position pos[a] on the pair's axis a turns by theta = pos[a] * w_p:
+//   (u, v) -> amp * (u cos theta - v sin theta, u sin theta + v cos theta)
+// (inverse: by -theta).  Channels past rope_dim are copied.  fp32 arithmetic, one rounding.
+//
+// Angles.  A turn is 2^64: F_p = round(w_p / 2 pi * 2^64), formed on the host, and pos * F_p
+// modulo 2^64 drops whole turns exactly, so a position of 2^31 costs no more accuracy than
+// position 1 (2^-33 turns from the rounding of F_p, 2^-25 of the angle from its conversion
+// to fp32).
+//
+// HBM-bound: x is read once and written once.  A thread owns 8 pairs of one token (16
+// channels, two 16-byte words of 16-bit values), takes their sines and cosines once and
+// applies them to all heads of its chunk, four heads' loads in flight at a time.
+#pragma once
+#include <cstdint>
+
+#include "residual_norm.cuh"  // unpack16, pack16
+
+namespace sba {
+
+constexpr int kMaxRotaryPairs = 128;
+
+struct RotaryParams {
+    const void* x;
+    void* out;
+    const int32_t* pos;                      // [B][N][axes]
+    long long x_sb, x_sh, x_sn, o_sb, o_sh, o_sn;  // strides in elements
+    int H, N, D, axes, pairs;
+    int heads_per_cta;
+    int half, copy, fp16;                    // copy: channels past rope_dim are written
+    float sin_amp, cos_amp;
+    unsigned long long turn[kMaxRotaryPairs];
+    unsigned char axis[kMaxRotaryPairs];
+};
+
+__device__ __forceinline__ void rotary_sincos(const RotaryParams& p, const int32_t* pos, int pair, float& s, float& c) {
+    const unsigned long long a = (unsigned long long)(long long)pos[p.axis[pair]] * p.turn[pair];
+    // the top 32 bits as a signed fraction of a turn; sincospif takes half turns
+    sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);
+    s *= p.sin_amp;
+    c *= p.cos_amp;
+}
+
+// Eight consecutive values, 16-byte accesses.
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> rotary_load(const char* q) {
+    Raw8<F32> r;
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) r.w[i] = ldg_stream(q + 16 * i);
+    return r;
+}
+template <bool F32>
+__device__ __forceinline__ void rotary_store(char* q, const float (&f)[8], int fp16) {
+    if (F32) {
+        stg_stream(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        stg_stream(q + 16, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                                      __float_as_uint(f[7])));
+    } else {
+        stg_stream(q, make_uint4(pack16(f[0], f[1], fp16), pack16(f[2], f[3], fp16), pack16(f[4], f[5], fp16),
+                                 pack16(f[6], f[7], fp16)));
+    }
+}
+
+// Vector form: D % 16 == 0, pairs % 8 == 0, rows 16-byte aligned.  256 threads: thread t
+// of the grid's x owns 16 channels of token t / (D / 16).
+template <bool F32>
+__global__ void __launch_bounds__(256) rotary_vec_kernel(const __grid_constant__ RotaryParams p) {
+    constexpr int W = F32 ? 4 : 2;
+    constexpr int U = F32 ? 2 : 4;  // heads in flight
+    const int tpt = p.D >> 4;       // threads per token
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int n = (int)(id / tpt), j = (int)(id % tpt);
+    if (n >= p.N) return;
+    const int b = blockIdx.z;
+    const int h0 = blockIdx.y * p.heads_per_cta;
+    const int h1 = min(p.H, h0 + p.heads_per_cta);
+    const bool turned = 8 * j < p.pairs;
+    if (!turned && !p.copy) return;
+    // the two runs of 8 channels
+    const int c0 = turned && p.half ? 8 * j : 16 * j;
+    const int c1 = turned && p.half ? p.pairs + 8 * j : 16 * j + 8;
+    const char* x = static_cast<const char*>(p.x) + (b * p.x_sb + n * p.x_sn) * W;
+    char* o = static_cast<char*>(p.out) + (b * p.o_sb + n * p.o_sn) * W;
+    float s[8], c[8];
+    if (turned) {
+        const int32_t* pos = p.pos + ((long long)b * p.N + n) * p.axes;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rotary_sincos(p, pos, 8 * j + e, s[e], c[e]);
+    }
+    for (int h = h0; h < h1; h += U) {
+        Raw8<F32> ra[U], rb[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (h + i < h1) {
+                ra[i] = rotary_load<F32>(x + ((h + i) * p.x_sh + c0) * W);
+                rb[i] = rotary_load<F32>(x + ((h + i) * p.x_sh + c1) * W);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (h + i >= h1) break;
+            float a[8], d[8];
+            raw_to_float<F32>(ra[i], p.fp16, a);
+            raw_to_float<F32>(rb[i], p.fp16, d);
+            if (turned && p.half) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float u = a[e], v = d[e];
+                    a[e] = fmaf(u, c[e], -v * s[e]);
+                    d[e] = fmaf(u, s[e], v * c[e]);
+                }
+            } else if (turned) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = a[2 * e], v = a[2 * e + 1], w = d[2 * e], z = d[2 * e + 1];
+                    a[2 * e] = fmaf(u, c[e], -v * s[e]);
+                    a[2 * e + 1] = fmaf(u, s[e], v * c[e]);
+                    d[2 * e] = fmaf(w, c[4 + e], -z * s[4 + e]);
+                    d[2 * e + 1] = fmaf(w, s[4 + e], z * c[4 + e]);
+                }
+            }
+            rotary_store<F32>(o + ((h + i) * p.o_sh + c0) * W, a, p.fp16);
+            rotary_store<F32>(o + ((h + i) * p.o_sh + c1) * W, d, p.fp16);
+        }
+    }
+}
+
+// Any size and alignment: a thread per (token, pair) or (token, copied channel).
+template <bool F32>
+__global__ void __launch_bounds__(256) rotary_any_kernel(const __grid_constant__ RotaryParams p) {
+    const int units = p.copy ? p.D - p.pairs : p.pairs;  // the pairs, then the copied channels
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long n = id / units;
+    const int j = (int)(id % units);
+    if (n >= p.N) return;
+    const int b = blockIdx.z;
+    const int h0 = blockIdx.y * p.heads_per_cta;
+    const int h1 = min(p.H, h0 + p.heads_per_cta);
+    const bool turned = j < p.pairs;
+    const int c0 = turned ? (p.half ? j : 2 * j) : p.pairs + j;
+    const int c1 = turned ? (p.half ? p.pairs + j : 2 * j + 1) : c0;
+    const long long xo = b * p.x_sb + n * p.x_sn, oo = b * p.o_sb + n * p.o_sn;
+    auto load = [&](long long at) {
+        if (F32) return static_cast<const float*>(p.x)[at];
+        float a, z;
+        unpack16(static_cast<const uint16_t*>(p.x)[at], p.fp16, a, z);
+        return a;
+    };
+    auto store = [&](long long at, float f) {
+        if (F32) static_cast<float*>(p.out)[at] = f;
+        else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack16(f, 0.f, p.fp16);
+    };
+    float s = 0.f, c = 1.f;
+    if (turned) rotary_sincos(p, p.pos + ((long long)b * p.N + n) * p.axes, j, s, c);
+    for (int h = h0; h < h1; ++h) {
+        const float u = load(xo + h * p.x_sh + c0);
+        if (!turned) {
+            store(oo + h * p.o_sh + c0, u);
+            continue;
+        }
+        const float v = load(xo + h * p.x_sh + c1);
+        store(oo + h * p.o_sh + c0, fmaf(u, c, -v * s));
+        store(oo + h * p.o_sh + c1, fmaf(u, s, v * c));
+    }
+}
+
+}  // namespace sba

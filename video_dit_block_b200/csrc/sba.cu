@@ -20,6 +20,9 @@
 #include "producer.cuh"
 #include "compensation.cuh"
 #include "prune.cuh"
+#include "residual_norm.cuh"
+#include "rotary.cuh"
+#include "int8_linear.cuh"
 
 namespace {
 
@@ -615,7 +618,7 @@ const char* sba_strerror(sba_status status) {
         case SBA_ERR_ALIGNMENT: return "misaligned device pointer";
         case SBA_ERR_CUDA: return "CUDA call failed";
         case SBA_ERR_TIMEOUT: return "a kernel wait gave up";
-        case SBA_ERR_DEVICE_FLAG: return "a kernel found an invalid routing entry";
+        case SBA_ERR_DEVICE_FLAG: return "a kernel found an invalid routing entry or index";
         case SBA_ERR_SCRATCH_TOO_SMALL: return "problem needs more scratch than the fixed no-allocation buffer holds";
     }
     return "unknown status";
@@ -779,4 +782,285 @@ extern "C" sba_status sba_pool_select_noalloc(const void* q, const void* k, int 
     if (st != SBA_OK) return st;
     return sba_pool_select(q, k, B, H, Npad, D, valid_len, block, sparsity, kmax, kv_idx, kv_cnt,
                            scratch, kNoAllocScratchBytes, stream);
+}
+
+// ---------------------------------------------------------------- the block around the attention
+namespace {
+
+bool is_dtype(int d) { return d == SBA_DTYPE_BF16 || d == SBA_DTYPE_FP16 || d == SBA_DTYPE_FP32; }
+int dtype_bytes(int d) { return d == SBA_DTYPE_FP32 ? 4 : 2; }
+bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+// Whether rows at p + i * stride elements all start on 16 bytes.
+bool rows16(const void* p, const int64_t* strides, int n, int width) {
+    if (!aligned16(p)) return false;
+    for (int i = 0; i < n; ++i)
+        if ((strides[i] * width) % 16 != 0) return false;
+    return true;
+}
+bool none_negative(const int64_t* s, int n) {
+    for (int i = 0; i < n; ++i)
+        if (s[i] < 0) return false;
+    return true;
+}
+
+template <bool X32, bool H32, int TPR, int VPT, bool VEC>
+sba_status launch_rows(const sba::RowParams& p, cudaStream_t s) {
+    constexpr int threads = TPR < 128 ? 128 : TPR, rpc = TPR < 128 ? 128 / TPR : 1;
+    sba::residual_norm_kernel<X32, H32, TPR, VPT, VEC><<<(unsigned)((p.rows + rpc - 1) / rpc), threads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
+}
+
+// The threads and chunks per row: the fewest registers that hold the row.
+template <bool X32, bool H32>
+sba_status run_rows(const sba::RowParams& p, bool vec, cudaStream_t s) {
+    const int chunks = p.quant ? p.Cq / 8 : (p.C + 7) / 8;
+    if (vec) {
+        if (chunks <= 32) return launch_rows<X32, H32, 32, 1, true>(p, s);
+        if (chunks <= 64) return launch_rows<X32, H32, 32, 2, true>(p, s);
+        if (chunks <= 128) return launch_rows<X32, H32, 32, 4, true>(p, s);
+        if (chunks <= 256) return launch_rows<X32, H32, 128, 2, true>(p, s);
+        if (chunks <= 384) return launch_rows<X32, H32, 128, 3, true>(p, s);
+        if (chunks <= 512) return launch_rows<X32, H32, 128, 4, true>(p, s);
+        if (chunks <= 640) return launch_rows<X32, H32, 128, 5, true>(p, s);
+        if (chunks <= 768) return launch_rows<X32, H32, 128, 6, true>(p, s);
+        if (chunks <= 1024) return launch_rows<X32, H32, 256, 4, true>(p, s);
+        if (chunks <= 2048) return launch_rows<X32, H32, 512, 4, true>(p, s);
+        return launch_rows<X32, H32, 512, 8, true>(p, s);
+    }
+    if (chunks <= 128) return launch_rows<X32, H32, 32, 4, false>(p, s);
+    if (chunks <= 1024) return launch_rows<X32, H32, 256, 4, false>(p, s);
+    return launch_rows<X32, H32, 512, 8, false>(p, s);
+}
+
+sba_status dispatch_rows(const sba::RowParams& p, int x_dtype, int dtype, bool vec, cudaStream_t s) {
+    if (x_dtype != SBA_DTYPE_FP32) return run_rows<false, false>(p, vec, s);
+    if (dtype != SBA_DTYPE_FP32) return run_rows<true, false>(p, vec, s);
+    return run_rows<true, true>(p, vec, s);
+}
+
+// Row-major [rows][K] 8-bit codes as a 2-D tensor; box = 128 codes x box_rows, 128-byte swizzle.
+bool make_map_codes(CUtensorMap* map, const void* base, long long rows, int K, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" sba_status sba_residual_norm(const void* x, const void* y, void* x_out, void* out, float* out_scale,
+                                        int x_dtype, int dtype, int B, int N, int C, const int64_t* strides,
+                                        const int32_t* valid_len, int norm, const void* weight, const void* bias,
+                                        int post_norm, const void* post_weight, const void* gate, const void* scale,
+                                        const void* shift, int param_dtype, int G, const int32_t* index, float eps,
+                                        void* stream) {
+    if (B <= 0 || N <= 0 || C <= 0) return SBA_ERR_INVALID_ARG;
+    if (!is_dtype(x_dtype) || !is_dtype(dtype) || !is_dtype(param_dtype)) return SBA_ERR_INVALID_ARG;
+    if (!x || !strides || !none_negative(strides, 8)) return SBA_ERR_INVALID_ARG;
+    if (norm < SBA_NORM_NONE || norm > SBA_NORM_RMS || post_norm < SBA_NORM_NONE || post_norm > SBA_NORM_RMS)
+        return SBA_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return SBA_ERR_INVALID_ARG;
+    // what a step without its operand would mean
+    if (y ? !x_out : (gate || post_norm || post_weight)) return SBA_ERR_INVALID_ARG;
+    if (norm ? !out : (!y || out_scale || weight || bias || scale || shift)) return SBA_ERR_INVALID_ARG;
+    if (post_weight && !post_norm) return SBA_ERR_INVALID_ARG;
+    const bool modulated = gate || scale || shift;
+    if (modulated && (G <= 0 || (!index && G < B))) return SBA_ERR_INVALID_ARG;
+    if (C > SBA_MAX_CHANNELS || (long long)B * N > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
+    if (x_dtype != dtype && x_dtype != SBA_DTYPE_FP32) return SBA_ERR_UNSUPPORTED;
+    if (param_dtype != SBA_DTYPE_FP32 && param_dtype != dtype) return SBA_ERR_UNSUPPORTED;
+    const int xw = dtype_bytes(x_dtype), hw = dtype_bytes(dtype), pw = dtype_bytes(param_dtype);
+    if (!aligned_to(x, xw) || !aligned_to(y, hw) || !aligned_to(x_out, xw) || !aligned_to(out, out_scale ? 16 : hw) ||
+        !aligned_to(out_scale, 4) || !aligned_to(weight, pw) || !aligned_to(bias, pw) || !aligned_to(post_weight, pw) ||
+        !aligned_to(gate, pw) || !aligned_to(scale, pw) || !aligned_to(shift, pw) || !aligned_to(index, 4) ||
+        !aligned_to(valid_len, 4))
+        return SBA_ERR_ALIGNMENT;
+    sba::RowParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x; p.y = y; p.r = x_out; p.h = out; p.h_scale = out_scale;
+    p.valid_len = valid_len;
+    p.index = modulated ? index : nullptr;
+    p.gate = gate; p.scale = scale; p.shift = shift;
+    p.weight = weight; p.bias = bias; p.post_weight = post_weight;
+    p.x_sb = strides[0]; p.x_sn = strides[1]; p.y_sb = strides[2]; p.y_sn = strides[3];
+    p.r_sb = strides[4]; p.r_sn = strides[5]; p.h_sb = strides[6]; p.h_sn = strides[7];
+    p.N = N; p.C = C; p.G = G;
+    p.rows = (long long)B * N;
+    p.norm = norm; p.post = post_norm; p.quant = out_scale != nullptr;
+    p.Cq = (C + 15) / 16 * 16;
+    if (p.quant && (p.h_sb % 16 || p.h_sn % 16)) return SBA_ERR_ALIGNMENT;
+    p.fp16 = dtype == SBA_DTYPE_FP16;
+    p.param32 = param_dtype == SBA_DTYPE_FP32;
+    p.eps = eps;
+    const bool vec = C % 8 == 0 && rows16(x, strides, 2, xw) && (!y || (rows16(y, strides + 2, 2, hw) &&
+                     rows16(x_out, strides + 4, 2, xw))) && (!norm || p.quant || rows16(out, strides + 6, 2, hw)) &&
+                     aligned16(weight) && aligned16(bias) && aligned16(post_weight) && aligned16(gate) &&
+                     aligned16(scale) && aligned16(shift);
+    return dispatch_rows(p, x_dtype, dtype, vec, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" sba_status sba_token_quantize(const void* x, int dtype, int B, int H, int N, int D, const int64_t* strides,
+                                         int8_t* codes, float* scales, void* stream) {
+    if (B <= 0 || H <= 0 || N <= 0 || D <= 0) return SBA_ERR_INVALID_ARG;
+    if (!is_dtype(dtype) || !x || !codes || !scales || !strides || !none_negative(strides, 3))
+        return SBA_ERR_INVALID_ARG;
+    if ((long long)H * D > SBA_MAX_CHANNELS || (long long)B * N > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
+    const int w = dtype_bytes(dtype);
+    if (!aligned_to(x, w) || !aligned16(codes) || !aligned_to(scales, 4)) return SBA_ERR_ALIGNMENT;
+    sba::RowParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x; p.h = codes; p.h_scale = scales;
+    p.x_sb = strides[0]; p.x_sh = strides[1]; p.x_sn = strides[2];
+    p.D = H > 1 ? D : 0;
+    p.N = N; p.C = H * D; p.G = 1;
+    p.Cq = (p.C + 15) / 16 * 16;
+    p.h_sn = p.Cq;
+    p.h_sb = (long long)N * p.Cq;
+    p.rows = (long long)B * N;
+    p.quant = 1;
+    p.fp16 = dtype == SBA_DTYPE_FP16;
+    const bool vec = D % 8 == 0 && rows16(x, strides, 3, w);
+    return dispatch_rows(p, dtype, dtype, vec, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
+                                      int B, int N, int K, int M, const void* bias, const void* gate, int param_dtype,
+                                      int G, const int32_t* index, int activation, const void* residual, void* out,
+                                      int out_dtype, int heads, const int64_t* strides, void* stream) {
+    if (B <= 0 || N <= 0 || K <= 0 || M <= 0 || heads < 0) return SBA_ERR_INVALID_ARG;
+    if (!a || !a_scale || !w || !w_scale || !out || !strides || !none_negative(strides, 5)) return SBA_ERR_INVALID_ARG;
+    if (!is_dtype(out_dtype) || !is_dtype(param_dtype)) return SBA_ERR_INVALID_ARG;
+    if (activation < SBA_ACT_NONE || activation > SBA_ACT_SILU) return SBA_ERR_INVALID_ARG;
+    if (heads > 0 && M % heads != 0) return SBA_ERR_INVALID_ARG;
+    if (gate && (G <= 0 || (!index && G < B))) return SBA_ERR_INVALID_ARG;
+    if (K % 16 != 0 || K > SBA_MAX_INT8_K) return SBA_ERR_UNSUPPORTED;
+    if (heads > 0 && (M / heads) % 32 != 0) return SBA_ERR_UNSUPPORTED;
+    if (param_dtype != SBA_DTYPE_FP32 && param_dtype != out_dtype) return SBA_ERR_UNSUPPORTED;
+    if ((long long)B * N > 0x7fffff00ll || M > (1 << 24)) return SBA_ERR_UNSUPPORTED;
+    const int ow = dtype_bytes(out_dtype), pw = dtype_bytes(param_dtype);
+    if (!aligned16(a) || !aligned16(w) || !aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, pw) ||
+        !aligned_to(gate, pw) || !aligned_to(residual, ow) || !aligned_to(out, ow) || !aligned_to(index, 4))
+        return SBA_ERR_ALIGNMENT;
+    sba::LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.a_scale = a_scale; p.w_scale = w_scale; p.bias = bias; p.gate = gate; p.residual = residual;
+    p.index = gate ? index : nullptr;
+    p.out = out;
+    p.res_sb = strides[0]; p.res_sn = strides[1];
+    p.out_sb = strides[2]; p.out_sh = strides[3]; p.out_sn = strides[4];
+    p.M = B * N; p.N = M; p.K = K;
+    p.tokens = N;
+    p.G = G;
+    p.D = heads > 0 ? M / heads : 0;
+    p.act = activation;
+    p.out_type = out_dtype;
+    p.param_type = param_dtype;
+    // column groups of 4 and 8 start on 16 bytes in every row
+    p.vec = aligned16(w_scale) && aligned16(bias) && rows16(out, strides + 2, 3, ow) &&
+            (!residual || rows16(residual, strides, 2, ow)) && (!gate || (aligned16(gate) && (long long)M * pw % 16 == 0));
+    p.wait_limit = g_wait_limit;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return SBA_ERR_CUDA;
+    CUtensorMap ta, tw;
+    const long long pair_tiles = ((p.M + 255ll) / 256) * ((p.N + 255ll) / 256);
+    if (pair_tiles > 0x3fffffffll) return SBA_ERR_UNSUPPORTED;
+    if (p.M > 128 && pair_tiles >= sms / 4) {
+        using SM = sba::PairSmem;
+        if (!make_map_codes(&ta, a, p.M, K, 128) || !make_map_codes(&tw, w, M, K, 128)) return SBA_ERR_CUDA;
+        if (cudaFuncSetAttribute(sba::int8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) !=
+            cudaSuccess)
+            return SBA_ERR_CUDA;
+        const int clusters = (int)(pair_tiles < sms / 2 ? pair_tiles : sms / 2);
+        sba::int8_pair_kernel<<<2 * clusters, sba::kPairThreads, SM::kAlloc, s>>>(ta, tw, p);
+        return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
+    }
+    using SM = sba::SplitSmem;
+    p.box_rows = p.M < 128 ? (p.M + 7) / 8 * 8 : 128;
+    if (!make_map_codes(&ta, a, p.M, K, p.box_rows) || !make_map_codes(&tw, w, M, K, SM::kBN)) return SBA_ERR_CUDA;
+    if (cudaFuncSetAttribute(sba::int8_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) !=
+        cudaSuccess)
+        return SBA_ERR_CUDA;
+    const int tiles_n = (p.N + SM::kBN - 1) / SM::kBN, tiles_m = (p.M + 127) / 128;
+    const int ksteps = (K + 127) / 128;
+    int splits = 1;
+    while (splits < 8 && 2 * splits * 4 <= ksteps && (long long)tiles_n * tiles_m * splits < 2 * sms) splits *= 2;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(tiles_n * splits), (unsigned)tiles_m);
+    cfg.blockDim = dim3(sba::kSplitThreads);
+    cfg.dynamicSmemBytes = SM::kAlloc;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sba::int8_split_kernel, ta, tw, p, splits) == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
+}
+
+extern "C" sba_status sba_rotary(const void* x, void* out, int dtype, const int32_t* pos, int axes, int B, int H, int N,
+                                 int D, const int64_t* strides, int rope_dim, int layout, const double* inv_freq,
+                                 const uint8_t* axis, float amplitude, int inverse, void* stream) {
+    if (B <= 0 || H <= 0 || N <= 0 || D <= 0 || axes <= 0 || axes > 255) return SBA_ERR_INVALID_ARG;
+    if (!is_dtype(dtype) || !x || !out || !pos || !strides || !inv_freq || !axis || !none_negative(strides, 6))
+        return SBA_ERR_INVALID_ARG;
+    if (layout != SBA_ROPE_INTERLEAVED && layout != SBA_ROPE_HALF) return SBA_ERR_INVALID_ARG;
+    if (rope_dim <= 0 || rope_dim > D || rope_dim % 2 != 0 || !std::isfinite(amplitude)) return SBA_ERR_INVALID_ARG;
+    if (rope_dim / 2 > sba::kMaxRotaryPairs || B > 65535 || H > 65535 || D > (1 << 20)) return SBA_ERR_UNSUPPORTED;
+    for (int i = 0; i < rope_dim / 2; ++i)
+        if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1e9 || axis[i] >= axes) return SBA_ERR_INVALID_ARG;
+    const int w = dtype_bytes(dtype);
+    if (!aligned_to(x, w) || !aligned_to(out, w) || !aligned_to(pos, 4)) return SBA_ERR_ALIGNMENT;
+    sba::RotaryParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x; p.out = out; p.pos = pos;
+    p.x_sb = strides[0]; p.x_sh = strides[1]; p.x_sn = strides[2];
+    p.o_sb = strides[3]; p.o_sh = strides[4]; p.o_sn = strides[5];
+    p.H = H; p.N = N; p.D = D; p.axes = axes; p.pairs = rope_dim / 2;
+    p.half = layout == SBA_ROPE_HALF;
+    p.copy = rope_dim < D && out != x;
+    p.fp16 = dtype == SBA_DTYPE_FP16;
+    p.cos_amp = amplitude;
+    p.sin_amp = inverse ? -amplitude : amplitude;
+    for (int i = 0; i < p.pairs; ++i) {
+        p.axis[i] = axis[i];
+        // turns a position, whole ones dropped, in 64 fractional bits
+        long double t = (long double)inv_freq[i] * 0.159154943091895335768883763372514362L;
+        t -= std::floor(t);
+        const long double scaled = std::floor(t * 18446744073709551616.0L + 0.5L);
+        p.turn[i] = scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
+    }
+    const bool vec = D % 16 == 0 && p.pairs % 8 == 0 && rows16(x, strides, 3, w) && rows16(out, strides + 3, 3, w);
+    const long long per_token = vec ? D / 16 : (p.copy ? D - p.pairs : p.pairs);
+    const long long gx = ((long long)N * per_token + 255) / 256;
+    if (gx > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return SBA_ERR_CUDA;
+    // heads a thread takes with one set of sines: eight, fewer when that leaves SMs idle
+    int hpc = 8;
+    while (hpc > 1 && gx * B * ((H + hpc - 1) / hpc) < 4ll * sms) hpc /= 2;
+    p.heads_per_cta = hpc;
+    const dim3 grid((unsigned)gx, (unsigned)((H + hpc - 1) / hpc), (unsigned)B);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (vec) {
+        if (dtype == SBA_DTYPE_FP32) sba::rotary_vec_kernel<true><<<grid, 256, 0, s>>>(p);
+        else sba::rotary_vec_kernel<false><<<grid, 256, 0, s>>>(p);
+    } else {
+        if (dtype == SBA_DTYPE_FP32) sba::rotary_any_kernel<true><<<grid, 256, 0, s>>>(p);
+        else sba::rotary_any_kernel<false><<<grid, 256, 0, s>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
 }

@@ -7,6 +7,7 @@ CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -100,6 +101,16 @@ def lib() -> ctypes.CDLL:
         L.sba_token_prune_select.argtypes = [vp, i32, i32, i32, vp, f64, i32, vp, vp, vp, sz, vp]
         L.sba_gather_tokens.restype = i32
         L.sba_gather_tokens.argtypes = [vp, i32, i32, i32, i32, vp, vp, i32, vp, vp]
+        L.sba_residual_norm.restype = i32
+        L.sba_residual_norm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp,
+                                        vp, i32, i32, vp, f32, vp]
+        L.sba_token_quantize.restype = i32
+        L.sba_token_quantize.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.sba_int8_linear.restype = i32
+        L.sba_int8_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i32, vp, i32, vp, vp, i32, i32, vp,
+                                      vp]
+        L.sba_rotary.restype = i32
+        L.sba_rotary.argtypes = [vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, i32, i32, vp, vp, f32, i32, vp]
         L.sba_strerror.restype = ctypes.c_char_p
         L.sba_strerror.argtypes = [i32]
         _lib = L
@@ -460,6 +471,328 @@ def gather_tokens(src, idx, valid_out, out=None, stream=None):
     _check(lib().sba_gather_tokens(_ptr(src), B, H, N, row_bytes, _ptr(idx), _ptr(valid_out), int(npad_out),
                                    _ptr(out), _stream(stream)), "sba_gather_tokens")
     return out
+
+
+# ---------------------------------------------------------------- the block around the attention
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_NORMS = {None: 0, "layer": 1, "rms": 2}
+_ACTS = {None: 0, "gelu_tanh": 1, "silu": 2}
+_LAYOUTS = {"interleaved": 0, "half": 1}
+_HERE = contextlib.nullcontext()
+
+
+def _place(t, stream):
+    """The context of a call on t's device: its allocations and launch on `stream`, or on
+    the device's current stream."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        if t.device.index == torch.cuda.current_device():
+            return _HERE
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _values(t, name, shape, device, dtypes):
+    """Check an optional tensor: shape, device, type, and contiguous unless `shape` is None."""
+    if t is None:
+        return
+    if t.device != device or t.dtype not in dtypes or (shape is not None and (
+            tuple(t.shape) != tuple(shape) or not t.is_contiguous())):
+        want = "" if shape is None else f" contiguous {tuple(shape)}"
+        raise ValueError(f"{name}: expected a{want} tensor on {device} of {' or '.join(str(d) for d in dtypes)}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _rows(t, name, shape, device, dtype, written=False):
+    """Check rows at any strides: the last dimension contiguous, and no two elements of a
+    written tensor in one place."""
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if written and not t.is_contiguous():
+        reach = 0
+        for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+            if stride <= reach:
+                raise ValueError(f"{name}: written elements overlap")
+            reach += stride * (size - 1)
+
+
+def _param_dtype(params, dtype, device, shapes):
+    """The one type of the parameters given (name, tensor) -- fp32 or `dtype` -- as a code."""
+    given = [(n, t) for n, t in params if t is not None]
+    if not given:
+        return 2
+    kind = given[0][1].dtype
+    if kind != torch.float32 and kind != dtype:
+        raise ValueError(f"{given[0][0]}: expected torch.float32 or {dtype}, got {kind}")
+    for n, t in given:
+        _values(t, n, shapes[n], device, (kind,))
+    return _DTYPES[kind]
+
+
+def _index_rows(index, tables, rows, B, device):
+    """Rows of the modulation tables: (their count, the index or None).  Without an index
+    sample b takes row b."""
+    sizes = {t.shape[0] if t.dim() == 2 else -1 for t in tables if t is not None}
+    if len(sizes) > 1 or -1 in sizes:
+        raise ValueError("gate, scale and shift must be [G, C] with one G")
+    G = sizes.pop() if sizes else 0
+    if index is None:
+        if G and G != B:
+            raise ValueError(f"{G} modulation rows for {B} samples, and no index")
+        return G
+    _values(index, "index", rows, device, (torch.int32,))
+    if not G:
+        raise ValueError("an index, and nothing that it selects from")
+    return G
+
+
+def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, scale=None, shift=None, index=None,
+                  post_norm=None, post_weight=None, valid_len=None, eps: float = 1e-6, quantize: bool = False,
+                  out_dtype=None, x_out=None, out=None, out_scale=None, stream=None):
+    """The gated residual of a block's output y, and the modulated norm of the new residual
+    stream, in one pass (see include/sba.h).
+
+      r = x + gate * post_norm(y) * post_weight
+      h = (norm(r) * weight + bias) * (1 + scale) + shift
+
+    x: [B, N, C] bf16, fp16 or fp32; y the same type, or 16-bit next to an fp32 x; both at
+    any strides with contiguous rows.  norm, post_norm: "layer", "rms" or None.  weight,
+    bias, post_weight: [C]; gate, scale, shift: [G, C], row b for sample b, or row
+    index[b, n] with an int32 index [B, N]; all fp32 or of h's type.  Rows past
+    valid_len[b] come out as zeros.
+
+    Returns (r, h); r is x itself when there is no y, h is None with norm=None.  With
+    quantize=True returns (r, codes, scales) for int8_linear: int8 [B, N, C rounded up to
+    16] and fp32 [B, N].  h has y's type (out_dtype without a y, x's by default).  x_out
+    may be x, out may be y."""
+    with _place(x, stream):
+        if x.dim() != 3 or x.dtype not in _DTYPES:
+            raise ValueError("x: expected [B, N, C] in bf16, fp16 or fp32")
+        B, N, C = x.shape
+        dev = x.device
+        dtype = y.dtype if y is not None else (out_dtype or x.dtype)
+        if dtype not in _DTYPES or (dtype != x.dtype and x.dtype != torch.float32) or (
+                out_dtype is not None and out_dtype != dtype):
+            raise ValueError(f"x of {x.dtype}, y of {None if y is None else y.dtype}, out_dtype {out_dtype}: h has y's "
+                             "type, and that is x's or, next to an fp32 x, 16-bit")
+        if norm not in _NORMS or post_norm not in _NORMS:
+            raise ValueError(f"norm {norm!r}, post_norm {post_norm!r}: each one of {sorted(map(str, _NORMS))}")
+        if norm is None and (quantize or y is None):
+            raise ValueError("norm=None needs a y, and gives nothing to quantize")
+        _rows(x, "x", (B, N, C), dev, x.dtype)
+        shapes = {"weight": (C,), "bias": (C,), "post_weight": (C,)}
+        G = _index_rows(index, (gate, scale, shift), (B, N), B, dev)
+        shapes.update(gate=(G, C), scale=(G, C), shift=(G, C))
+        ptype = _param_dtype((("weight", weight), ("bias", bias), ("post_weight", post_weight), ("gate", gate),
+                              ("scale", scale), ("shift", shift)), dtype, dev, shapes)
+        _values(valid_len, "valid_len", (B,), dev, (torch.int32,))
+        strides = [x.stride(0), x.stride(1), 0, 0, 0, 0, 0, 0]
+        if y is not None:
+            _rows(y, "y", (B, N, C), dev, dtype)
+            if x_out is None:
+                x_out = torch.empty((B, N, C), dtype=x.dtype, device=dev)
+            _rows(x_out, "x_out", (B, N, C), dev, x.dtype, written=True)
+            strides[2:6] = y.stride(0), y.stride(1), x_out.stride(0), x_out.stride(1)
+        elif x_out is not None:
+            raise ValueError("x_out without a y: the residual stream does not change")
+        if norm is not None:
+            shape, kind = ((B, N, -(-C // 16) * 16), torch.int8) if quantize else ((B, N, C), dtype)
+            if out is None:
+                out = torch.empty(shape, dtype=kind, device=dev)
+            _rows(out, "out", shape, dev, kind, written=True)
+            strides[6:8] = out.stride(0), out.stride(1)
+            if quantize and out_scale is None:
+                out_scale = torch.empty((B, N), dtype=torch.float32, device=dev)
+            if quantize:
+                _values(out_scale, "out_scale", (B, N), dev, (torch.float32,))
+        elif out is not None:
+            raise ValueError("out without a norm")
+        if out_scale is not None and not quantize:
+            raise ValueError("out_scale without quantize")
+        if B and N:
+            _check(lib().sba_residual_norm(
+                _ptr(x), _ptr(y), _ptr(x_out), _ptr(out), _ptr(out_scale), _DTYPES[x.dtype], _DTYPES[dtype], B, N, C,
+                (ctypes.c_int64 * 8)(*strides), _ptr(valid_len), _NORMS[norm], _ptr(weight), _ptr(bias),
+                _NORMS[post_norm], _ptr(post_weight), _ptr(gate), _ptr(scale), _ptr(shift), ptype, G, _ptr(index),
+                float(eps), _stream(stream)), "sba_residual_norm")
+        r = x if y is None else x_out
+        return (r, out, out_scale) if quantize else (r, out)
+
+
+def token_quantize(x, codes=None, scales=None, stream=None):
+    """Rows in 8 bits with one scale a row: scales = max|row| / 127, codes the nearest integers
+    (see include/sba.h).  x: [..., K] of bf16, fp16 or fp32, [M, K] (tokens, or a weight's
+    output channels), [B, N, K], or the attention's head layout [B, H, N, D], whose K = H * D;
+    at any strides with contiguous rows.  Returns (codes int8 [M, K'] or [B, N, K'], scales
+    fp32 [M] or [B, N]), K' = K rounded up to a multiple of 16 (zero codes)."""
+    with _place(x, stream):
+        if x.dim() not in (2, 3, 4) or x.dtype not in _DTYPES or (x.stride(-1) != 1 and x.shape[-1] > 1):
+            raise ValueError("x: expected [M, K], [B, N, K] or [B, H, N, D] in bf16, fp16 or fp32, its last dimension "
+                             "contiguous")
+        if x.dim() == 4:
+            (B, H, N, D), (sb, sh, sn) = x.shape, x.stride()[:3]
+        elif x.dim() == 3:
+            (B, N, D), (sb, sn), H, sh = x.shape, x.stride()[:2], 1, 0
+        else:
+            (N, D), sn, B, H, sb, sh = x.shape, x.stride(0), 1, 1, 0, 0
+        lead = (N,) if x.dim() == 2 else (B, N)
+        width = -(-(H * D) // 16) * 16
+        if codes is None:
+            codes = torch.empty((*lead, width), dtype=torch.int8, device=x.device)
+        if scales is None:
+            scales = torch.empty(lead, dtype=torch.float32, device=x.device)
+        _values(codes, "codes", (*lead, width), x.device, (torch.int8,))
+        _values(scales, "scales", lead, x.device, (torch.float32,))
+        if B and N:
+            _check(lib().sba_token_quantize(_ptr(x), _DTYPES[x.dtype], B, H, N, D, (ctypes.c_int64 * 3)(sb, sh, sn),
+                                            _ptr(codes), _ptr(scales), _stream(stream)), "sba_token_quantize")
+        return codes, scales
+
+
+def int8_linear(codes, scales, weight_codes, weight_scales, bias=None, activation=None, gate=None, index=None,
+                residual=None, out_dtype=torch.bfloat16, heads=None, out=None, stream=None):
+    """A projection in 8-bit integers with its epilogue (see include/sba.h):
+
+      out = residual + gate * activation((codes @ weight_codes.T) * scales * weight_scales + bias)
+
+    codes int8 [N, K] or [B, N, K] and scales fp32 [N] or [B, N] as residual_norm and
+    token_quantize give them; weight_codes int8 [M, K] and weight_scales fp32 [M]
+    (token_quantize of the weight).  activation: None, "gelu_tanh" or "silu".  bias: [M];
+    gate: [G, M], row b for sample b or row index[b, n]; both fp32 or of out's type.
+    residual: of out's shape and type, contiguous rows, may be out.  Returns out [..., M]; with
+    heads=H (and codes [B, N, K]) the attention's layout [B, H, N, M / H] instead."""
+    with _place(codes, stream):
+        dev = codes.device
+        if codes.dim() not in (2, 3) or codes.dtype != torch.int8 or not codes.is_contiguous():
+            raise ValueError("codes: expected a contiguous int8 tensor [N, K] or [B, N, K]")
+        lead, K = tuple(codes.shape[:-1]), codes.shape[-1]
+        B, N = lead if codes.dim() == 3 else (1, *lead)
+        if weight_codes.dim() != 2:
+            raise ValueError("weight_codes: expected [M, K]")
+        M = weight_codes.shape[0]
+        _values(scales, "scales", lead, dev, (torch.float32,))
+        _values(weight_codes, "weight_codes", (M, K), dev, (torch.int8,))
+        _values(weight_scales, "weight_scales", (M,), dev, (torch.float32,))
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out_dtype {out_dtype}: expected bf16, fp16 or fp32")
+        if activation not in _ACTS:
+            raise ValueError(f"unknown activation {activation!r}; one of {sorted(map(str, _ACTS))}")
+        if heads is not None and (codes.dim() != 3 or heads < 1 or M % heads or residual is not None):
+            raise ValueError("heads: codes [B, N, K], a divisor of M, and no residual")
+        G = _index_rows(index, (gate,), lead, B, dev)
+        ptype = _param_dtype((("bias", bias), ("gate", gate)), out_dtype, dev, {"bias": (M,), "gate": (G, M)})
+        shape = (B, heads, N, M // heads) if heads else (*lead, M)
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=dev)
+        _rows(out, "out", shape, dev, out_dtype, written=True)
+        strides = [0] * 5
+        if residual is not None:
+            _rows(residual, "residual", shape, dev, out_dtype)
+            strides[:2] = residual.stride()[:2] if len(lead) == 2 else (0, residual.stride(0))
+        if heads:
+            strides[2:] = out.stride()[:3]
+        else:
+            strides[2:] = (out.stride(0), 0, out.stride(1)) if len(lead) == 2 else (0, 0, out.stride(0))
+        if B and N:
+            _check(lib().sba_int8_linear(
+                _ptr(codes), _ptr(scales), _ptr(weight_codes), _ptr(weight_scales), B, N, K, M, _ptr(bias), _ptr(gate),
+                ptype, G, _ptr(index), _ACTS[activation], _ptr(residual), _ptr(out), _DTYPES[out_dtype], heads or 0,
+                (ctypes.c_int64 * 5)(*strides), _stream(stream)), "sba_int8_linear")
+        return out
+
+
+class RopeTable:
+    """The frequencies of `rotary`: radians a position and the position axis of each of
+    rope_dim / 2 channel pairs, and the factor on the turned channels."""
+
+    def __init__(self, inv_freq, axis=None, amplitude: float = 1.0):
+        self.inv_freq = tuple(float(f) for f in inv_freq)
+        self.axis = tuple(int(a) for a in axis) if axis is not None else (0,) * len(self.inv_freq)
+        self.amplitude = float(amplitude)
+        n = len(self.inv_freq)
+        if n == 0 or len(self.axis) != n or min(self.axis) < 0 or max(self.axis) > 254:
+            raise ValueError("one axis in 0..254 for each pair's frequency, and a pair at least")
+        if not all(math.isfinite(f) for f in self.inv_freq) or not math.isfinite(self.amplitude):
+            raise ValueError("frequencies and amplitude must be finite")
+        self.rope_dim = 2 * n
+        self.axes = max(self.axis) + 1
+        self._freq = (ctypes.c_double * n)(*self.inv_freq)
+        self._axis = (ctypes.c_uint8 * n)(*self.axis)
+
+
+def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scaling=None, factor: float = 1.0,
+                     original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0) -> RopeTable:
+    """The usual frequencies base^(-2i/d) of rope_dim channels split evenly into `axes` axes
+    of d channels each, for positions past the trained length scaled by `factor`:
+
+      None      as they are
+      "linear"  every frequency / factor
+      "ntk"     base * factor^(d / (d - 2)) in place of base
+      "yarn"    pairs that turn at least beta_fast times within original_length positions as
+                they are, those that turn at most beta_slow times / factor, a linear ramp over
+                the pairs between; amplitude 0.1 ln(factor) + 1"""
+    if axes < 1 or rope_dim < 2 or rope_dim % (2 * axes):
+        raise ValueError("rope_dim must split into an even number of channels an axis")
+    if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive and finite")
+    d = rope_dim // axes
+    amplitude = 1.0
+    if scaling == "ntk":
+        if d == 2:
+            raise ValueError("ntk scaling needs more than one pair an axis")
+        base = base * factor ** (d / (d - 2))
+    freq = [base ** (-2.0 * i / d) for i in range(d // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if base == 1 or original_length < 1 or not 0 < beta_slow < beta_fast:
+            raise ValueError("yarn scaling: base != 1, original_length >= 1 and 0 < beta_slow < beta_fast")
+        # the pair index that turns `turns` times within the original length
+        pair = lambda turns: d * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), d - 1)
+        ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(d // 2)]
+        freq = [f / factor * t + f * (1 - t) for f, t in zip(freq, ramp)]
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return RopeTable(freq * axes, [a for a in range(axes) for _ in range(d // 2)], amplitude)
+
+
+def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool = False, out=None, stream=None):
+    """Rotary positions (see include/sba.h): the first table.rope_dim channels of x [B, H, N, D]
+    turned by the token's position, the others copied.  x: bf16, fp16 or fp32 at any strides
+    with contiguous channels (a token-major [B, N, H, D] tensor is x.transpose(1, 2)).  pos:
+    int32 [B, N, table.axes], or [B, N] for one axis.  layout: pairs of channels (2p, 2p + 1),
+    "interleaved", or (p, p + rope_dim / 2), "half".  inverse turns back, which is also the
+    gradient.  out may be x.  Returns out (laid out as x)."""
+    with _place(x, stream):
+        if x.dim() != 4 or x.dtype not in _DTYPES:
+            raise ValueError("x: expected [B, H, N, D] in bf16, fp16 or fp32")
+        B, H, N, D = x.shape
+        if layout not in _LAYOUTS:
+            raise ValueError(f"unknown layout {layout!r}; one of {sorted(_LAYOUTS)}")
+        if table.rope_dim > D:
+            raise ValueError(f"a table of {table.rope_dim} channels for heads of {D}")
+        _rows(x, "x", x.shape, x.device, x.dtype)
+        shape = (B, N) if pos.dim() == 2 and table.axes == 1 else (B, N, table.axes)
+        _values(pos, "pos", shape, x.device, (torch.int32,))
+        if out is None:
+            out = torch.empty_like(x)
+        _rows(out, "out", x.shape, x.device, x.dtype, written=True)
+        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+            raise ValueError("out at x's place with other strides")
+        if B and H and N:
+            _check(lib().sba_rotary(_ptr(x), _ptr(out), _DTYPES[x.dtype], _ptr(pos), table.axes, B, H, N, D,
+                                    (ctypes.c_int64 * 6)(*x.stride()[:3], *out.stride()[:3]), table.rope_dim,
+                                    _LAYOUTS[layout], ctypes.addressof(table._freq), ctypes.addressof(table._axis),
+                                    table.amplitude, int(inverse), _stream(stream)), "sba_rotary")
+        return out
 
 
 def device_status(stream=None) -> int:
