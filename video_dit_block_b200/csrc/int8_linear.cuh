@@ -13,10 +13,10 @@
 //   int8_pair_kernel  large products.  A cluster of two CTAs computes tiles of 256 x 256:
 //                     cta_group::2 MMAs of M = 256, each CTA staging its 128 rows of A and
 //                     its 128 rows of W, which halves the shared-memory traffic of W and
-//                     leaves 64 bytes a clock of the 128.  Persistent: the accumulators of
+//                     leaves it 64 bytes a clock of the 128.  Persistent: the accumulators of
 //                     two tiles alternate in TMEM, so the eight epilogue warps finish one
 //                     tile while the MMAs of the next run.
-//   int8_split_kernel few rows or few tiles.  One CTA per 128 x 64 tile and K split; the
+//   int8_split_kernel few rows or few tiles.  One CTA per tile of 128 x bn and K split; the
 //                     splits of a tile form a cluster and add their integer sums through
 //                     distributed shared memory (exact in any order).  With few rows it
 //                     streams W once: HBM-bound.
@@ -51,6 +51,8 @@ struct LinearParams {
     int act;
     int out_type, param_type;  // 0 bf16, 1 fp16, 2 fp32
     int vec;                   // rows and parameters allow 16-byte accesses
+    int bn;                    // columns of a tile: 64, 128, 192 or 256 (split kernel: 64 or 128)
+    int stages;                // K steps in flight
     int box_rows;              // rows of A loaded per tile (split kernel)
     unsigned long long wait_limit;
 };
@@ -83,6 +85,52 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// A tiled load whose bytes count on a barrier of either CTA of the pair (given by its
+// shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+// The count goes ahead of the loads it announces and carries no data of this thread, so it is
+// relaxed: a release at cluster scope made the producer wait for its loads (0.8 us a step
+// in place of 0.3).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// True in one lane of a converged warp, the same one every time.  The MMAs and loads are issued
+// behind it, from loops that the whole warp runs: behind `lane == 0` the compiler cannot know that
+// one lane is left, and an MMA took 180 cycles to issue whatever its size; behind this it takes
+// 80, less than a 128 x 256 x 32 needs (128).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// A bounded wait by polling whose outcome is the same, and known to be the same, for the whole
+// warp.
+__device__ __forceinline__ bool warp_poll_bounded(uint32_t bar, uint32_t parity, volatile uint32_t* abort,
+                                                  uint64_t limit) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+        bool stop = *abort != 0;
+        if ((uint64_t)(clock64() - t0) > limit) {
+            if (!stop) raise_device_error(kErrTimeout);
+            *abort = 1u;
+            stop = true;
+        }
+        if (__any_sync(0xffffffffu, stop)) return false;
+    }
+}
+
 // ------------------------------------------------------------------- epilogue
 // What an output row needs.
 struct LinearRow {
@@ -111,40 +159,49 @@ __device__ __forceinline__ LinearRow linear_row(const LinearParams& p, int m) {
     return r;
 }
 
-// U values (4 or 8) of type `type` at column n of a row.
+// U parameters (4 or 8) of type `type` at column n of a row.
 template <int U>
 __device__ __forceinline__ void linear_load(float (&f)[U], const char* row, int n, int type) {
-    if (type == 2) {
+    if (U > 8) {
+#pragma unroll
+        for (int i = 0; i < U; i += 8) {
+            float g[8];
+            linear_load<8>(g, row, n + i, type);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[(i + e) % U] = g[e];
+        }
+    } else if (type == 2) {
 #pragma unroll
         for (int i = 0; i < U; i += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + 4ll * (n + i));
+            const float4 a = __ldg(reinterpret_cast<const float4*>(row + 4ll * (n + i)));
             f[i] = a.x; f[i + 1] = a.y; f[i + 2] = a.z; f[i + 3] = a.w;
         }
     } else if (U == 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(row + 2ll * n);
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + 2ll * n));
         unpack16(w.x, type, f[0], f[1]);
         unpack16(w.y, type, f[2], f[3]);
         unpack16(w.z, type, f[U - 4], f[U - 3]);
         unpack16(w.w, type, f[U - 2], f[U - 1]);
+    } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + 2ll * n));
+        unpack16(w.x, type, f[0], f[1]);
+        unpack16(w.y, type, f[2], f[3]);
+    }
+}
+// Four values of a row of residuals (which may be the output: plain loads) or outputs.
+__device__ __forceinline__ void linear_read4(float (&f)[4], const char* row, int n, int type) {
+    if (type == 2) {
+        const float4 a = *reinterpret_cast<const float4*>(row + 4ll * n);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     } else {
         const uint2 w = *reinterpret_cast<const uint2*>(row + 2ll * n);
         unpack16(w.x, type, f[0], f[1]);
         unpack16(w.y, type, f[2], f[3]);
     }
 }
-template <int U>
-__device__ __forceinline__ void linear_store(char* row, long long n, const float (&f)[U], int type) {
-    if (type == 2) {
-#pragma unroll
-        for (int i = 0; i < U; i += 4)
-            *reinterpret_cast<float4*>(row + 4 * (n + i)) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-    } else if (U == 8) {
-        *reinterpret_cast<uint4*>(row + 2 * n) = make_uint4(pack16(f[0], f[1], type), pack16(f[2], f[3], type),
-                                                            pack16(f[U - 4], f[U - 3], type),
-                                                            pack16(f[U - 2], f[U - 1], type));
-    } else {
-        *reinterpret_cast<uint2*>(row + 2 * n) = make_uint2(pack16(f[0], f[1], type), pack16(f[2], f[3], type));
-    }
+__device__ __forceinline__ void linear_write4(char* row, long long n, const float (&f)[4], int type) {
+    if (type == 2) *reinterpret_cast<float4*>(row + 4 * n) = make_float4(f[0], f[1], f[2], f[3]);
+    else *reinterpret_cast<uint2*>(row + 2 * n) = make_uint2(pack16(f[0], f[1], type), pack16(f[2], f[3], type));
 }
 __device__ __forceinline__ float linear_load1(const void* base, long long i, int type) {
     if (type == 2) return static_cast<const float*>(base)[i];
@@ -153,64 +210,84 @@ __device__ __forceinline__ float linear_load1(const void* base, long long i, int
     return a;
 }
 
+// v * sigmoid(t): silu takes t = v, the tanh form of GELU t = 2 sqrt(2/pi) (v + 0.044715 v^3).
+// -t log2(e) is formed directly; an exponential that overflows ends in v * (1 / inf) = 0.
 __device__ __forceinline__ float linear_act(float v, int act) {
     if (act == kActNone) return v;
-    // v * sigmoid(t): silu takes t = v, the tanh form of GELU t = 2 sqrt(2/pi) (v + 0.044715 v^3)
-    const float t = act == kActSilu ? v : v * fmaf(0.07135481282052155f, v * v, 1.5957691216057308f);
-    return __fdividef(v, 1.f + __expf(-fmaxf(t, -80.f)));
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float t = act == kActSilu ? -kLog2e * v
+                                    : v * fmaf(-0.07135481282052155f * kLog2e, v * v, -1.5957691216057308f * kLog2e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(t)));
+    return v * r;
 }
 
-// Columns n .. n + U - 1 of a row whose accumulators are `acc`, all of them inside N.
+// v of columns n .. n + U - 1 of a row, before the residual; `sw` and `bias` are those
+// columns' (bias 0 where there is none).
 template <int U>
-__device__ __forceinline__ void linear_finish(const LinearParams& p, const LinearRow& r, int n, const int* acc) {
-    float v[U], t[U];
-    linear_load<U>(t, reinterpret_cast<const char*>(p.w_scale), n, 2);
+__device__ __forceinline__ void linear_value(float (&v)[U], const LinearParams& p, const LinearRow& r, int n,
+                                             const uint32_t* acc, const float* sw, const float* bias) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) v[i] = (float)acc[i] * (r.sa * t[i]);
-    if (p.bias) {
-        linear_load<U>(t, static_cast<const char*>(p.bias), n, p.param_type);
-#pragma unroll
-        for (int i = 0; i < U; ++i) v[i] += t[i];
+    for (int i = 0; i < U; i += 4) {
+        float4 s = make_float4(sw[0], sw[1], sw[2], sw[3]), b = make_float4(bias[0], bias[1], bias[2], bias[3]);
+        if (U > 4) {  // from shared memory, aligned
+            s = *reinterpret_cast<const float4*>(sw + i);
+            b = *reinterpret_cast<const float4*>(bias + i);
+        }
+        v[i] = fmaf((float)(int)acc[i], r.sa * s.x, b.x);
+        v[i + 1] = fmaf((float)(int)acc[i + 1], r.sa * s.y, b.y);
+        v[i + 2] = fmaf((float)(int)acc[i + 2], r.sa * s.z, b.z);
+        v[i + 3] = fmaf((float)(int)acc[i + 3], r.sa * s.w, b.w);
     }
     if (p.act) {
 #pragma unroll
         for (int i = 0; i < U; ++i) v[i] = linear_act(v[i], p.act);
     }
     if (r.gate) {
+        float t[U];
         linear_load<U>(t, r.gate, n, p.param_type);
 #pragma unroll
         for (int i = 0; i < U; ++i) v[i] *= t[i];
     }
-    if (r.res) {
-        linear_load<U>(t, r.res, n, p.out_type);
-#pragma unroll
-        for (int i = 0; i < U; ++i) v[i] += t[i];
-    }
-    linear_store<U>(r.out, p.D ? (n / p.D) * p.out_sh + n % p.D : (long long)n, v, p.out_type);
+}
+// The offset of column n in its output row.
+__device__ __forceinline__ long long linear_col(const LinearParams& p, int n) {
+    return p.D ? (n / p.D) * p.out_sh + n % p.D : (long long)n;
 }
 // One column, any alignment.
 __device__ __forceinline__ void linear_finish1(const LinearParams& p, const LinearRow& r, int n, int acc) {
-    float v = (float)acc * (r.sa * p.w_scale[n]);
-    if (p.bias) v += linear_load1(p.bias, n, p.param_type);
-    v = linear_act(v, p.act);
+    const float bias = p.bias ? linear_load1(p.bias, n, p.param_type) : 0.f;
+    float v = linear_act(fmaf((float)acc, r.sa * p.w_scale[n], bias), p.act);
     if (r.gate) v *= linear_load1(r.gate, n, p.param_type);
     if (r.res) v += linear_load1(r.res, n, p.out_type);
-    const long long at = p.D ? (n / p.D) * p.out_sh + n % p.D : (long long)n;
+    const long long at = linear_col(p, n);
     if (p.out_type == 2) reinterpret_cast<float*>(r.out)[at] = v;
     else reinterpret_cast<uint16_t*>(r.out)[at] = (uint16_t)pack16(v, 0.f, p.out_type);
 }
 
 // ------------------------------------------------------------------- large products
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+constexpr int kMaxStages = 10;
 struct PairSmem {
-    static constexpr int kStages = 6;
-    static constexpr int kABytes = 128 * 128, kWBytes = 128 * 128;
-    static constexpr int kStageBytes = kABytes + kWBytes;
-    static constexpr int kBars = kStages * kStageBytes;
-    // barriers: full[6], peer[6], empty[6], acc_full[2], acc_empty[2], drain
-    static constexpr int kNumBars = 3 * kStages + 5;
-    static constexpr int kCtl = kBars + kNumBars * 8;
+    static constexpr int kABytes = 128 * 128;  // 128 rows of A, then bn / 2 of W, a stage
+    static constexpr int kRing = 6 * 32768;    // the operand ring: as many stages as fit
+    // barriers: full[10], empty[10], acc_full[2], acc_empty[2], drain
+    static constexpr int kBars = kRing;
+    static constexpr int kCols = kBars + (2 * kMaxStages + 6) / 2 * 16;  // float [2 tiles][scale, bias][256]
+    static constexpr int kOut = kCols + 2 * 2 * 256 * 4;                 // 2 KB an epilogue warp
+    static constexpr int kCtl = kOut + 8 * 2048;
     static constexpr int kAlloc = kCtl + 16 + 1024;
+    static __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn / 2 * 128; }
+    static __host__ __device__ constexpr int stages(int bn) {
+        return kRing / stage_bytes(bn) < kMaxStages ? kRing / stage_bytes(bn) : kMaxStages;
+    }
 };
+static_assert(PairSmem::kAlloc <= 227 * 1024, "one CTA's shared memory");
 constexpr int kPairThreads = 320;
 constexpr int kPairGroup = 8;  // row tiles that walk the columns together
 
@@ -225,12 +302,84 @@ __device__ __forceinline__ void pair_tile(int i, int tiles_m, int tiles_n, int& 
     tn = j / rows;
 }
 
+// A lane of an epilogue warp has a row of the accumulator, but 32 lanes storing to 32 rows
+// take 32 cycles an access and held the tile back (11,600 cycles a tile; 25,000 with a
+// residual).  So the rows pass through 2 KB of shared memory in pieces of 64 bytes a row
+// (32 columns of 16 bits, 16 of fp32), and four lanes move one row's piece.  16-byte word j of row r
+// stands at 4 r + (j ^ (r / 2 & 3)): eight lanes touch all banks either way.
+__device__ __forceinline__ int pair_word(int r, int j) { return 4 * r + (j ^ ((r >> 1) & 3)); }
+
+// The residual of the piece at column n, as this lane moves it.
+__device__ __forceinline__ void pair_fetch(uint4 (&res)[4], const LinearParams& p, const long long (&row)[4],
+                                           const bool (&live)[4], int n, int lane) {
+    const char* base = static_cast<const char*>(p.residual) + 16 * (lane & 3);
+    const int w = p.out_type == 2 ? 4 : 2;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (live[r]) res[r] = *reinterpret_cast<const uint4*>(base + (row[r] + n) * w);
+}
+
+// One piece from the accumulators of the lane's row to the output.
+template <bool F32>
+__device__ __forceinline__ void pair_piece(const LinearParams& p, const LinearRow& row, int n, const uint32_t* acc,
+                                           const float* s_col, bool any_res, const uint4 (&res)[4], uint4* stage,
+                                           const long long (&out_row)[4], const bool (&live)[4], int lane) {
+    constexpr int U = F32 ? 16 : 32;
+    float v[U];
+    linear_value<U>(v, p, row, n, acc, s_col, s_col + 256);
+    if (any_res) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) stage[pair_word(8 * r + (lane >> 2), lane & 3)] = res[r];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 w = stage[pair_word(lane, j)];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (F32) {
+                    v[4 * j + e] += __uint_as_float(u[e]);
+                } else {
+                    float a, b;
+                    unpack16(u[e], p.out_type, a, b);
+                    v[U / 4 * j + 2 * e] += a;
+                    v[U / 4 * j + 2 * e + 1] += b;
+                }
+            }
+        }
+    }
+    // each word of the stage is rewritten by the lane that has just read it
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint4 w;
+        if (F32) {
+            w = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                           __float_as_uint(v[4 * j + 3]));
+        } else {
+            const float* f = v + U / 4 * j;
+            w = make_uint4(pack16(f[0], f[1], p.out_type), pack16(f[2], f[3], p.out_type),
+                           pack16(f[4 % (U / 4)], f[5 % (U / 4)], p.out_type),
+                           pack16(f[6 % (U / 4)], f[7 % (U / 4)], p.out_type));
+        }
+        stage[pair_word(lane, j)] = w;
+    }
+    __syncwarp();
+    const long long col = linear_col(p, n);
+    char* base = static_cast<char*>(p.out) + 16 * (lane & 3);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint4 w = stage[pair_word(8 * r + (lane >> 2), lane & 3)];
+        if (live[r]) *reinterpret_cast<uint4*>(base + (out_row[r] + col) * (F32 ? 4 : 2)) = w;
+    }
+    __syncwarp();
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ LinearParams p) {
     using SM = PairSmem;
-    constexpr int NS = SM::kStages;
-    constexpr uint32_t kIdesc = idesc_s8_s32(256, 256);
+    const int NS = p.stages, kStage = SM::stage_bytes(p.bn);
+    const uint32_t idesc = idesc_s8_s32(256, p.bn);
     constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
     constexpr uint16_t kBoth = 0x3;
     extern __shared__ unsigned char smem_raw[];
@@ -238,18 +387,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(sm), bars = base + SM::kBars;
     auto bar_full = [&](int s) { return bars + 8u * s; };
-    auto bar_peer = [&](int s) { return bars + 8u * (NS + s); };
-    auto bar_empty = [&](int s) { return bars + 8u * (2 * NS + s); };
-    auto bar_af = [&](int s) { return bars + 8u * (3 * NS + s); };
-    auto bar_ae = [&](int s) { return bars + 8u * (3 * NS + 2 + s); };
-    const uint32_t bar_drain = bars + 8u * (3 * NS + 4);
+    auto bar_empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
+    auto bar_af = [&](int s) { return bars + 8u * (2 * kMaxStages + s); };
+    auto bar_ae = [&](int s) { return bars + 8u * (2 * kMaxStages + 2 + s); };
+    const uint32_t bar_drain = bars + 8u * (2 * kMaxStages + 4);
     uint32_t* ctl = reinterpret_cast<uint32_t*>(sm + SM::kCtl);
     volatile uint32_t* abort_flag = ctl + 1;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = (int)cluster_ctarank();
     const bool leader = rank == 0;
-    const int tiles_m = (p.M + 255) / 256, tiles_n = (p.N + 255) / 256;
+    const int tiles_m = (p.M + 255) / 256, tiles_n = (p.N + p.bn - 1) / p.bn;
+    const int wr = p.bn / 2;  // rows of W a CTA stages, and columns an epilogue warp finishes
     const int tiles = tiles_m * tiles_n;
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int ksteps = (p.K + 127) / 128;
@@ -257,8 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(bar_full(s), 1);
-            mbar_init(bar_peer(s), 1);
+            mbar_init(bar_full(s), 2);  // CTA 0's counts both CTAs' loads
             mbar_init(bar_empty(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -273,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = ctl[0];
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl[0], 0);
     int issued = 0;  // stages whose loads the producer has issued
 
     if (warp == 8) {
@@ -281,103 +429,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (lane == 0) {
             tma_prefetch_desc(&tmA);
             tma_prefetch_desc(&tmW);
-            bool ok = true;
-            for (int i = first; ok && i < tiles; i += step) {
-                int tm, tn;
-                pair_tile(i, tiles_m, tiles_n, tm, tn);
-                const int ra = tm * 256 + rank * 128, rw = tn * 256 + rank * 128;
-                for (int k = 0; k < ksteps; ++k) {
-                    const int st = issued % NS;
-                    if (issued >= NS && !wait_bounded(bar_empty(st), ((issued / NS) - 1) & 1, abort_flag, lim)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(bar_full(st), SM::kStageBytes);
-                    tma_load_2d(base + st * SM::kStageBytes, &tmA, bar_full(st), k * 128, ra);
-                    tma_load_2d(base + st * SM::kStageBytes + SM::kABytes, &tmW, bar_full(st), k * 128, rw);
-                    ++issued;
+        }
+        bool ok = true;
+        int st = 0;          // stage, and the parity of its next wait
+        uint32_t par = 1;
+        for (int i = first; ok && i < tiles; i += step) {
+            int tm, tn;
+            pair_tile(i, tiles_m, tiles_n, tm, tn);
+            const int ra = tm * 256 + rank * 128, rw = tn * p.bn + rank * wr;
+            for (int k = 0; k < ksteps; ++k) {
+                if (issued >= NS && !warp_poll_bounded(bar_empty(st), par, abort_flag, lim)) {
+                    ok = false;
+                    break;
                 }
+                if (elect_one()) {
+                    const uint32_t full = mapa_shared(bar_full(st), 0);
+                    mbar_arrive_expect_tx_cluster(full, SM::kABytes + wr * 128);
+                    tma_load_2d_pair(base + st * kStage, &tmA, full, k * 128, ra);
+                    tma_load_2d_pair(base + st * kStage + SM::kABytes, &tmW, full, k * 128, rw);
+                }
+                ++issued;
+                if (++st == NS) st = 0, par ^= 1;
             }
         }
     } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer (pair)
         if (leader) {
-            // -------------------------------------------------------- MMA issuer (pair)
-            if (lane == 0) {
-                const uint64_t da = smem_desc_sw128(base, 16, 1024);
-                const uint64_t dw = smem_desc_sw128(base + SM::kABytes, 16, 1024);
-                constexpr uint64_t kStep = SM::kStageBytes >> 4;
-                bool ok = true;
-                int it = 0, done = 0;
-                for (int i = first; ok && i < tiles; i += step, ++done) {
-                    const int buf = done & 1;
-                    if (done >= 2 && !poll_bounded(bar_ae(buf), ((done >> 1) - 1) & 1, abort_flag, lim)) break;
-                    tc_fence_after();
-                    for (int k = 0; k < ksteps; ++k, ++it) {
-                        const int st = it % NS;
-                        const uint32_t par = (it / NS) & 1;
-                        if (!poll_bounded(bar_full(st), par, abort_flag, lim) ||
-                            !poll_bounded(bar_peer(st), par, abort_flag, lim)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)  // 32 codes an instruction
-                            mma_pair_s8_ss(tmem + buf * 256, da + st * kStep + 2 * kk, dw + st * kStep + 2 * kk, kIdesc,
-                                           (k > 0 || kk > 0) ? 1u : 0u);
-                        mma_pair_commit(bar_empty(st), kBoth);
-                    }
-                    if (ok) mma_pair_commit(bar_af(buf), kBoth);
-                }
-            }
-        } else if (lane == 0) {
-            // -------------------------------------------------------- relay (CTA 1)
-            // CTA 0's MMAs read this CTA's operands: tell it when each stage has landed.
-            int it = 0;
+            const uint64_t da = smem_desc_sw128(base, 16, 1024);
+            const uint64_t dw = smem_desc_sw128(base + SM::kABytes, 16, 1024);
+            const uint64_t step16 = (uint64_t)(kStage >> 4);
             bool ok = true;
-            for (int i = first; ok && i < tiles; i += step) {
-                for (int k = 0; k < ksteps; ++k, ++it) {
-                    const int st = it % NS;
-                    if (!wait_bounded(bar_full(st), (it / NS) & 1, abort_flag, lim)) {
+            int st = 0, done = 0;
+            uint32_t par = 0;
+            uint64_t sa = da, sw = dw;
+            for (int i = first; ok && i < tiles; i += step, ++done) {
+                const int buf = done & 1;
+                if (done >= 2 && !warp_poll_bounded(bar_ae(buf), ((done >> 1) - 1) & 1, abort_flag, lim)) break;
+                tc_fence_after();
+                for (int k = 0; k < ksteps; ++k) {
+                    if (!warp_poll_bounded(bar_full(st), par, abort_flag, lim)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_remote(mapa_shared(bar_peer(st), 0));
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)  // 32 codes an instruction
+                            mma_pair_s8_ss(tmem + buf * 256, sa + 2 * kk, sw + 2 * kk, idesc,
+                                           (k > 0 || kk > 0) ? 1u : 0u);
+                        mma_pair_commit(bar_empty(st), kBoth);
+                    }
+                    __syncwarp();
+                    sa += step16, sw += step16;
+                    if (++st == NS) st = 0, par ^= 1, sa = da, sw = dw;
                 }
+                if (ok && elect_one()) mma_pair_commit(bar_af(buf), kBoth);
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue warps
+        // (the four warps of a half pass the same named barriers whatever happens: a wait that
+        // fails is carried to the end of its tile)
         const int quad = warp & 3, half = warp >> 2;
         int done = 0;
+        bool failed = false;
+        uint4* stage = reinterpret_cast<uint4*>(sm + SM::kOut) + warp * 128;
         for (int i = first; i < tiles; i += step, ++done) {
             const int buf = done & 1;
             int tm, tn;
             pair_tile(i, tiles_m, tiles_n, tm, tn);
             const int m = tm * 256 + rank * 128 + quad * 32 + lane;
-            const int n0 = tn * 256 + half * 128;
-            LinearRow row;
-            if (m < p.M) row = linear_row(p, m);
-            if (!warp_wait_bounded(bar_af(buf), (done >> 1) & 1, abort_flag, lim)) break;
+            const int n0 = tn * p.bn + half * wr;
+            const LinearRow row = linear_row(p, m < p.M ? m : p.M - 1);
+            // while the MMAs run: the columns' scales and biases into shared memory, the first
+            // piece of the residual into registers
+            float* s_col = reinterpret_cast<float*>(sm + SM::kCols) + buf * 512 + half * 128;
+            {
+                const int c = quad * 32 + lane, n = n0 + c;
+                const bool in = c < wr && n < p.N;
+                s_col[c] = in ? p.w_scale[n] : 0.f;
+                s_col[256 + c] = in && p.bias ? linear_load1(p.bias, n, p.param_type) : 0.f;
+            }
+            // the rows this lane moves: 8 i + lane / 4, 16 bytes at lane % 4 of each 64-byte piece
+            long long out_row[4], res_row[4];
+            bool live[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int mr = tm * 256 + rank * 128 + quad * 32 + 8 * r + (lane >> 2);
+                const int b = mr / p.tokens, tk = mr - b * p.tokens;
+                live[r] = mr < p.M;
+                out_row[r] = b * p.out_sb + tk * p.out_sn;
+                res_row[r] = b * p.res_sb + tk * p.res_sn;
+            }
+            named_bar_sync(1 + half, 128);
+            uint4 res[4];
+            const bool any_res = p.vec && p.residual;
+            if (any_res && n0 + 32 <= p.N) pair_fetch(res, p, res_row, live, n0, lane);
+            if (!warp_wait_bounded(bar_af(buf), (done >> 1) & 1, abort_flag, lim)) failed = true;
             tc_fence_after();
-            const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256 + half * 128;
+            const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256 + half * wr;
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
+            for (int ch = 0; 32 * ch < wr; ++ch) {
                 uint32_t acc[32];
-                __syncwarp();
+                const int n = n0 + 32 * ch;
                 tmem_ld32(tl + 32 * ch, acc);
                 tmem_wait_ld();
-                const int n = n0 + 32 * ch;
-                if (m >= p.M || n >= p.N) continue;
-                const int* ai = reinterpret_cast<const int*>(acc);
+                if (failed || n >= p.N) continue;  // the same for the whole warp
                 if (p.vec && n + 32 <= p.N) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) linear_finish<8>(p, row, n + 8 * q, ai + 8 * q);
-                } else {
+                    const bool more = any_res && 32 * ch + 32 < wr && n + 64 <= p.N;
+                    if (p.out_type == 2) {
+                        pair_piece<true>(p, row, n, acc, s_col + 32 * ch, any_res, res, stage, out_row, live, lane);
+                        if (any_res) pair_fetch(res, p, res_row, live, n + 16, lane);
+                        pair_piece<true>(p, row, n + 16, acc + 16, s_col + 32 * ch + 16, any_res, res, stage, out_row,
+                                         live, lane);
+                    } else {
+                        pair_piece<false>(p, row, n, acc, s_col + 32 * ch, any_res, res, stage, out_row, live, lane);
+                    }
+                    if (more) pair_fetch(res, p, res_row, live, n + 32, lane);
+                } else if (m < p.M) {
 #pragma unroll
                     for (int q = 0; q < 32; ++q)
-                        if (n + q < p.N) linear_finish1(p, row, n + q, ai[q]);
+                        if (n + q < p.N) linear_finish1(p, row, n + q, (int)acc[q]);
                 }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -387,14 +561,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     // ---------------------------------------------------------------- teardown
     __syncwarp();
+    if (warp == 8 && lane == 0) ctl[2] = (uint32_t)issued;
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag) {
-        // this CTA's own copies land, and CTA 0's MMAs finish, before TMEM is freed
-        if (warp == 8 && lane == 0) {
-            for (int t = issued > NS ? issued - NS : 0; t < issued; ++t) wait_drain(bar_full(t % NS), (t / NS) & 1);
+    cluster_sync();
+    // After an abort in either CTA both CTAs' loads land, and CTA 0's MMAs finish, before TMEM
+    // is freed.  All roles are done, so the counts of loads stand; a stage that only one CTA
+    // has loaded is completed by an arrival in the other's place.
+    const bool aborted = ld_cluster_u32(mapa_shared(smem_u32(ctl + 1), 0)) | ld_cluster_u32(mapa_shared(smem_u32(ctl + 1), 1));
+    if (aborted) {
+        if (warp == 8 && lane == 0 && leader) {
+            const int own = issued, peer = (int)ld_cluster_u32(mapa_shared(smem_u32(ctl + 2), 1));
+            const int most = own > peer ? own : peer;
+            for (int t = most > NS ? most - NS : 0; t < most; ++t) {
+                if (t >= own || t >= peer) mbar_arrive(bar_full(t % NS));
+                wait_drain(bar_full(t % NS), (t / NS) & 1);
+            }
         }
-        if (warp == 9 && lane == 0 && leader) {
+        if (warp == 9 && leader && elect_one()) {  // the lane that issued the MMAs
             mma_pair_commit_local(bar_drain);
             wait_drain(bar_drain, 0);
         }
@@ -409,16 +593,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------------------------- few rows or tiles
+// The MMAs read 128 rows of A a stage, but only the rows that exist are loaded, so with few
+// rows the stages of A stand box_rows apart and each one's unused rows are its neighbours':
+// their sums are never read.  W's stages come first, then A's, then room for the last one.
 struct SplitSmem {
-    static constexpr int kStages = 3, kBN = 64;
-    static constexpr int kABytes = 128 * 128, kWBytes = kBN * 128;
-    static constexpr int kStageBytes = kABytes + kWBytes;
-    static constexpr int kPitch = kBN * 4 + 16;  // bytes a row of the staged sums
-    static constexpr int kBars = kStages * kStageBytes;
-    static constexpr int kCtl = kBars + (2 * kStages + 2) * 8;
-    static constexpr int kAlloc = kCtl + 16 + 1024;
-    static_assert(128 * kPitch <= kBars, "the sums are staged over the operand ring");
+    static constexpr int kBars = 0;  // full[10], empty[10], acc, drain
+    static constexpr int kCtl = (2 * kMaxStages + 2) * 8;
+    static constexpr int kRing = 1024;
+    static __host__ __device__ constexpr int stage_bytes(int bn, int box) { return (bn + box) * 128; }
+    static __host__ __device__ constexpr int pitch(int bn) { return bn * 4 + 16; }  // bytes a row of the staged sums
+    static __host__ __device__ constexpr int alloc(int bn, int box, int stages) {
+        const int ring = stages * stage_bytes(bn, box) + (128 - box) * 128, sums = box * pitch(bn);
+        return kRing + (ring > sums ? ring : sums) + 1024;
+    }
 };
+static_assert(SplitSmem::kCtl + 16 <= SplitSmem::kRing, "barriers before the ring");
 constexpr int kSplitThreads = 192;
 
 __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
@@ -436,26 +625,27 @@ __global__ void __launch_bounds__(kSplitThreads) int8_split_kernel(const __grid_
                                                                    const __grid_constant__ CUtensorMap tmW,
                                                                    const __grid_constant__ LinearParams p, int splits) {
     using SM = SplitSmem;
-    constexpr int NS = SM::kStages, BN = SM::kBN;
-    constexpr uint32_t kIdesc = idesc_s8_s32(128, BN);
+    const int NS = p.stages, BN = p.bn;
+    const uint32_t idesc = idesc_s8_s32(128, BN);
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const uint32_t base = smem_u32(sm), bars = base + SM::kBars;
+    const uint32_t bars = smem_u32(sm) + SM::kBars, ring = smem_u32(sm) + SM::kRing;
     auto bar_full = [&](int s) { return bars + 8u * s; };
-    auto bar_empty = [&](int s) { return bars + 8u * (NS + s); };
-    const uint32_t bar_acc = bars + 8u * (2 * NS), bar_drain = bars + 8u * (2 * NS + 1);
+    auto bar_empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
+    const uint32_t bar_acc = bars + 8u * (2 * kMaxStages), bar_drain = bars + 8u * (2 * kMaxStages + 1);
     uint32_t* ctl = reinterpret_cast<uint32_t*>(sm + SM::kCtl);
     volatile uint32_t* abort_flag = ctl + 1;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
     const int n0 = (int)(blockIdx.x / splits) * BN, m0 = (int)blockIdx.y * 128;
     const int rows = min(128, p.M - m0);
     const int ksteps = (p.K + 127) / 128;
     const int k0 = (int)((long long)ksteps * rank / splits), k1 = (int)((long long)ksteps * (rank + 1) / splits);
     const uint64_t lim = p.wait_limit;
-    const uint32_t bytes = (uint32_t)p.box_rows * 128 + SM::kWBytes;
+    const int w_bytes = BN * 128, a_bytes = p.box_rows * 128, pitch = SM::pitch(BN);
+    const uint32_t ring_a = ring + NS * w_bytes;
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -471,7 +661,7 @@ __global__ void __launch_bounds__(kSplitThreads) int8_split_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ctl[0];
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl[0], 0);
     int issued = 0;
     bool ok = true;
 
@@ -479,48 +669,56 @@ __global__ void __launch_bounds__(kSplitThreads) int8_split_kernel(const __grid_
         if (lane == 0) {
             tma_prefetch_desc(&tmA);
             tma_prefetch_desc(&tmW);
-            for (int k = k0; k < k1; ++k) {
-                const int st = issued % NS;
-                if (issued >= NS && !wait_bounded(bar_empty(st), ((issued / NS) - 1) & 1, abort_flag, lim)) break;
-                // rows of A past box_rows stay as they are: their sums are never read
-                mbar_arrive_expect_tx(bar_full(st), bytes);
-                tma_load_2d(base + st * SM::kStageBytes + SM::kABytes, &tmW, bar_full(st), k * 128, n0);
-                tma_load_2d(base + st * SM::kStageBytes, &tmA, bar_full(st), k * 128, m0);
-                ++issued;
+        }
+        int st = 0;          // stage, and the parity of its next wait
+        uint32_t par = 1;
+        for (int k = k0; k < k1; ++k) {
+            if (issued >= NS && !warp_poll_bounded(bar_empty(st), par, abort_flag, lim)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar_full(st), (uint32_t)(w_bytes + a_bytes));
+                tma_load_2d(ring + st * w_bytes, &tmW, bar_full(st), k * 128, n0);
+                tma_load_2d(ring_a + st * a_bytes, &tmA, bar_full(st), k * 128, m0);
             }
+            ++issued;
+            if (++st == NS) st = 0, par ^= 1;
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            const uint64_t da = smem_desc_sw128(base, 16, 1024);
-            const uint64_t dw = smem_desc_sw128(base + SM::kABytes, 16, 1024);
-            constexpr uint64_t kStep = SM::kStageBytes >> 4;
-            for (int it = 0; it < k1 - k0; ++it) {
-                const int st = it % NS;
-                if (!poll_bounded(bar_full(st), (it / NS) & 1, abort_flag, lim)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+        const uint64_t da = smem_desc_sw128(ring_a, 16, 1024), dw = smem_desc_sw128(ring, 16, 1024);
+        const uint64_t step_a = (uint64_t)(a_bytes >> 4), step_w = (uint64_t)(w_bytes >> 4);
+        int st = 0;
+        uint32_t par = 0;
+        uint64_t sa = da, sw = dw;
+        for (int k = k0; k < k1; ++k) {
+            if (!warp_poll_bounded(bar_full(st), par, abort_flag, lim)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_s8_ss(tmem, da + st * kStep + 2 * kk, dw + st * kStep + 2 * kk, kIdesc,
-                              (it > 0 || kk > 0) ? 1u : 0u);
+                    mma_s8_ss(tmem, sa + 2 * kk, sw + 2 * kk, idesc, (k > k0 || kk > 0) ? 1u : 0u);
                 mma_commit(bar_empty(st));
             }
-            if (ok) mma_commit(bar_acc);
+            __syncwarp();
+            sa += step_a, sw += step_w;
+            if (++st == NS) st = 0, par ^= 1, sa = da, sw = dw;
         }
+        if (ok && elect_one()) mma_commit(bar_acc);
     } else if (warp * 32 < rows) {
         ok = warp_wait_bounded(bar_acc, 0, abort_flag, lim);
         tc_fence_after();
         if (ok) {
             // every MMA is done, so the operand ring is free
-            unsigned char* dst = sm + (warp * 32 + lane) * SM::kPitch;
+            unsigned char* dst = sm + SM::kRing + (warp * 32 + lane) * pitch;
+            const bool stored = warp * 32 + lane < rows;
             const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-#pragma unroll
             for (int ch = 0; ch < BN / 32; ++ch) {
                 uint32_t acc[32];
+                __syncwarp();
                 tmem_ld32(tl + 32 * ch, acc);
                 tmem_wait_ld();
+                if (!stored) continue;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     *reinterpret_cast<uint4*>(dst + 128 * ch + 16 * q) =
@@ -535,7 +733,7 @@ __global__ void __launch_bounds__(kSplitThreads) int8_split_kernel(const __grid_
         if (warp == 4 && lane == 0) {
             for (int t = issued > NS ? issued - NS : 0; t < issued; ++t) wait_drain(bar_full(t % NS), (t / NS) & 1);
         }
-        if (warp == 5 && lane == 0) {
+        if (warp == 5 && elect_one()) {  // the lane that issued the MMAs
             mma_commit(bar_drain);
             wait_drain(bar_drain, 0);
         }
@@ -545,30 +743,46 @@ __global__ void __launch_bounds__(kSplitThreads) int8_split_kernel(const __grid_
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, BN);
 
-    // the splits' sums, four columns a thread, the tile's items dealt over the cluster
-    if (!*abort_flag) {
-        const int items = rows * (BN / 4);
-        for (int i = rank * kSplitThreads + tid; i < items; i += splits * kSplitThreads) {
-            const int r = i / (BN / 4), c = 4 * (i % (BN / 4));
-            const int n = n0 + c;
-            if (n >= p.N) continue;
-            const uint32_t at = base + r * SM::kPitch + c * 4;
-            int acc[4] = {0, 0, 0, 0};
+    // the splits' sums: a thread keeps four columns, whose parameters it loads once, and walks the
+    // rows that are dealt over the cluster
+    const int groups = BN / 4, rows_at_once = kSplitThreads / groups;
+    const int c = 4 * (tid % groups), n = n0 + c;
+    if (!*abort_flag && n < p.N) {
+        const bool whole = p.vec && n + 4 <= p.N;
+        float sw[4], bias[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            sw[q] = n + q < p.N ? p.w_scale[n + q] : 0.f;
+            bias[q] = p.bias && n + q < p.N ? linear_load1(p.bias, n + q, p.param_type) : 0.f;
+        }
+        const long long col = linear_col(p, n);
+#pragma unroll 2
+        for (int r = rank * rows_at_once + tid / groups; r < rows; r += splits * rows_at_once) {
+            const LinearRow row = linear_row(p, m0 + r);
+            float res[4];
+            if (whole && row.res) linear_read4(res, row.res, n, p.out_type);
+            const uint32_t at = ring + r * pitch + c * 4;
+            uint32_t acc[4] = {0, 0, 0, 0};
             for (int s = 0; s < splits; ++s) {
                 const int4 v = splits > 1 ? ld_cluster_int4(mapa_shared(at, s))
-                                          : *reinterpret_cast<const int4*>(sm + r * SM::kPitch + c * 4);
+                                          : *reinterpret_cast<const int4*>(sm + SM::kRing + r * pitch + c * 4);
                 acc[0] += v.x;
                 acc[1] += v.y;
                 acc[2] += v.z;
                 acc[3] += v.w;
             }
-            const LinearRow row = linear_row(p, m0 + r);
-            if (p.vec && n + 4 <= p.N) {
-                linear_finish<4>(p, row, n, acc);
+            if (whole) {
+                float v[4];
+                linear_value<4>(v, p, row, n, acc, sw, bias);
+                if (row.res) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] += res[q];
+                }
+                linear_write4(row.out, col, v, p.out_type);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (n + q < p.N) linear_finish1(p, row, n + q, acc[q]);
+                    if (n + q < p.N) linear_finish1(p, row, n + q, (int)acc[q]);
             }
         }
     }

@@ -16,9 +16,12 @@
 // from registers, so a large common offset costs no digits.
 //
 // HBM-bound: x and y are read once, r and h written once; a row stays in the registers of
-// its TPR threads (VPT chunks of 8 channels each), all its loads issued before the first
-// use.  The parameter rows are shared by all rows of a sample and come from L1: they are
-// the only loads that may allocate there, the streams bypass it.
+// its threads, VPT chunks of 8 channels each, all its loads issued before the first use.
+// CTAs stay and walk the rows, the next row's loads in flight under this one's arithmetic.
+// Rows of up to 1024 channels take a warp, wider ones a CTA of as many warps as they need.
+// Arithmetic is in packed pairs: at 29 instructions a channel an earlier form was bound by
+// issue, not by memory.  The parameter rows are shared by all rows of a sample and come from
+// L1: they are the only loads that may allocate there, the streams bypass it.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -51,7 +54,6 @@ struct RowParams {
     int Cq;                    // quantised: code columns, C rounded up to 16
     long long rows;            // B * N
     int norm, post, quant;
-    int fp16;                  // 16-bit values are fp16 (else bf16)
     int param32;               // parameters are fp32 (else the 16-bit type)
     float eps;
 };
@@ -92,137 +94,167 @@ __device__ __forceinline__ void stg_stream(void* p, const uint4& v) {
                  : "memory");
 }
 
-// Eight values of a row as loaded: one 16-byte word of 16-bit values, or two of fp32.
-template <bool F32>
+// How a kernel holds its rows.  T: 0 bf16, 1 fp16, 2 fp32.
+enum RowType : int { kRowBf16 = 0, kRowFp16 = 1, kRowFp32 = 2 };
+
+// Where element e of chunk v of thread t stands: with VEC eight neighbours per thread,
+// otherwise (rows whose address or length rules 16-byte accesses out) one neighbour per
+// thread, so that a warp's single-element accesses coalesce.  tpr: threads of a row.
+template <bool VEC>
+__device__ __forceinline__ int row_col(int v, int t, int tpr, int e) {
+    return VEC ? (v * tpr + t) * 8 + e : (v * 8 + e) * tpr + t;
+}
+
+// Eight values of a row as loaded: one 16-byte word of 16-bit values, two of fp32; without
+// VEC a 32-bit word each.
+template <int T, bool VEC>
 struct Raw8 {
-    uint4 w[F32 ? 2 : 1];
+    static constexpr int kWords = T == kRowFp32 || !VEC ? 2 : 1;
+    uint4 w[kWords];
 };
 
-// The column of element e of chunk v of thread t: with VEC eight neighbours per thread,
-// otherwise (rows whose address or length rules 16-byte accesses out) one neighbour per
-// thread, so that a warp's single-element accesses coalesce.
-template <int TPR, bool VEC>
-__device__ __forceinline__ int row_col(int v, int t, int e) {
-    return VEC ? (v * TPR + t) * 8 + e : (v * 8 + e) * TPR + t;
+// A thread's place in its row.  `live`: with VEC, its chunks that lie in the row (the first
+// ones: C is a multiple of 8 there).
+struct RowPlace {
+    int t, tpr, C, live;
+};
+template <bool VEC>
+__device__ __forceinline__ bool row_has(const RowPlace& q, int v, int e) {
+    return VEC ? v < q.live : row_col<false>(v, q.t, q.tpr, e) < q.C;
 }
 
-template <bool F32, int TPR, bool VEC>
-__device__ __forceinline__ void row_load(Raw8<F32>& raw, const void* base, int v, int t, int C) {
-    constexpr int W = F32 ? 4 : 2;
+// Columns past C give zeros.
+template <int T, bool VEC>
+__device__ __forceinline__ void row_load(Raw8<T, VEC>& raw, const char* base, int v, const RowPlace& q) {
+    constexpr int W = T == kRowFp32 ? 4 : 2;
     if (VEC) {
-        const int c = row_col<TPR, true>(v, t, 0);
-        if (c < C) {
-            const char* p = static_cast<const char*>(base) + (long long)c * W;
-            raw.w[0] = ldg_stream(p);
-            if (F32) raw.w[F32 ? 1 : 0] = ldg_stream(p + 16);
-        }
+        const char* p = base + (v * q.tpr + q.t) * (8 * W);
+#pragma unroll
+        for (int i = 0; i < Raw8<T, VEC>::kWords; ++i)
+            raw.w[i] = v < q.live ? ldg_stream(p + 16 * i) : make_uint4(0, 0, 0, 0);
     } else {
-        uint32_t u[F32 ? 8 : 4];
+        uint32_t u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = row_col<TPR, false>(v, t, e);
-            uint32_t val = 0;
-            if (c < C) val = F32 ? static_cast<const uint32_t*>(base)[c] : static_cast<const uint16_t*>(base)[c];
-            if (F32) u[F32 ? e : 0] = val;
-            else if (e & 1) u[e >> 1] |= val << 16;
-            else u[e >> 1] = val;
+            const int c = row_col<false>(v, q.t, q.tpr, e);
+            u[e] = 0;
+            if (c < q.C)
+                u[e] = W == 4 ? reinterpret_cast<const uint32_t*>(base)[c] : reinterpret_cast<const uint16_t*>(base)[c];
         }
         raw.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        if (F32) raw.w[F32 ? 1 : 0] = make_uint4(u[F32 ? 4 : 0], u[F32 ? 5 : 0], u[F32 ? 6 : 0], u[F32 ? 7 : 0]);
+        raw.w[Raw8<T, VEC>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
 }
 
-template <bool F32>
-__device__ __forceinline__ void raw_to_float(const Raw8<F32>& raw, int fp16, float (&f)[8]) {
-    if (F32) {
-        const uint4 a = raw.w[0], b = raw.w[F32 ? 1 : 0];
-        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// As four packed pairs of floats.
+template <int T, bool VEC>
+__device__ __forceinline__ void row_values(const Raw8<T, VEC>& raw, uint64_t (&f)[4]) {
+    const uint4 a = raw.w[0], b = raw.w[Raw8<T, VEC>::kWords - 1];
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[e]);
-    } else {
-        const uint32_t u[4] = {raw.w[0].x, raw.w[0].y, raw.w[0].z, raw.w[0].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) unpack16(u[e], fp16, f[2 * e], f[2 * e + 1]);
-    }
-}
-
-// Eight parameters of the same columns, through L1.  Columns past C give 0.
-template <int TPR, bool VEC>
-__device__ __forceinline__ void param_load(float (&f)[8], const void* base, int param32, int fp16, int v, int t, int C) {
-    if (VEC) {
-        const int c = row_col<TPR, true>(v, t, 0);
-        if (c >= C) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 0.f;
-        } else if (param32) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + c);
-            const float4 a = __ldg(p), b = __ldg(p + 1);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi, none;
+        if (T == kRowFp32) {
+            lo = __uint_as_float(u[2 * i]);
+            hi = __uint_as_float(u[2 * i + 1]);
+        } else if (VEC) {
+            unpack16(u[i], T, lo, hi);
         } else {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + c));
-            unpack16(w.x, fp16, f[0], f[1]);
-            unpack16(w.y, fp16, f[2], f[3]);
-            unpack16(w.z, fp16, f[4], f[5]);
-            unpack16(w.w, fp16, f[6], f[7]);
+            unpack16(u[2 * i], T, lo, none);
+            unpack16(u[2 * i + 1], T, hi, none);
+        }
+        f[i] = pack2(lo, hi);
+    }
+}
+
+template <int T, bool VEC>
+__device__ __forceinline__ void row_store(char* base, const uint64_t (&f)[4], int v, const RowPlace& q) {
+    constexpr int W = T == kRowFp32 ? 4 : 2;
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(f[i], g[2 * i], g[2 * i + 1]);
+    if (VEC) {
+        if (v >= q.live) return;
+        char* p = base + (v * q.tpr + q.t) * (8 * W);
+        if (T == kRowFp32) {
+            stg_stream(p, make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                                     __float_as_uint(g[3])));
+            stg_stream(p + 16, make_uint4(__float_as_uint(g[4]), __float_as_uint(g[5]), __float_as_uint(g[6]),
+                                          __float_as_uint(g[7])));
+        } else {
+            stg_stream(p, make_uint4(pack16(g[0], g[1], T), pack16(g[2], g[3], T), pack16(g[4], g[5], T),
+                                     pack16(g[6], g[7], T)));
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = row_col<TPR, false>(v, t, e);
-            float a = 0.f, b;
-            if (c < C) {
-                if (param32) a = __ldg(static_cast<const float*>(base) + c);
-                else unpack16(__ldg(static_cast<const uint16_t*>(base) + c), fp16, a, b);
+            const int c = row_col<false>(v, q.t, q.tpr, e);
+            if (c >= q.C) continue;
+            if (T == kRowFp32) reinterpret_cast<float*>(base)[c] = g[e];
+            else reinterpret_cast<uint16_t*>(base)[c] = (uint16_t)pack16(g[e], 0.f, T);
+        }
+    }
+}
+
+// Eight parameters of the same columns, through L1: fp32, or 16-bit of type T16.  Columns past
+// C give 0.
+template <int T16, bool VEC>
+__device__ __forceinline__ void param_load(uint64_t (&f)[4], const char* base, int param32, int v, const RowPlace& q) {
+    float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (VEC) {
+        if (v < q.live) {
+            if (param32) {
+                // 32 bytes at once: two loads of 16 at a stride of 32 would each touch every line
+                asm("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                    : "=f"(g[0]), "=f"(g[1]), "=f"(g[2]), "=f"(g[3]), "=f"(g[4]), "=f"(g[5]), "=f"(g[6]), "=f"(g[7])
+                    : "l"(base + (v * q.tpr + q.t) * 32));
+            } else {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(base + (v * q.tpr + q.t) * 16));
+                unpack16(w.x, T16, g[0], g[1]);
+                unpack16(w.y, T16, g[2], g[3]);
+                unpack16(w.z, T16, g[4], g[5]);
+                unpack16(w.w, T16, g[6], g[7]);
             }
-            f[e] = a;
-        }
-    }
-}
-
-template <bool F32, int TPR, bool VEC>
-__device__ __forceinline__ void row_store(void* base, const float (&f)[8], int fp16, int v, int t, int C) {
-    if (VEC) {
-        const int c = row_col<TPR, true>(v, t, 0);
-        if (c >= C) return;
-        if (F32) {
-            float* p = static_cast<float*>(base) + c;
-            stg_stream(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                     __float_as_uint(f[3])));
-            stg_stream(p + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                                         __float_as_uint(f[7])));
-        } else {
-            stg_stream(static_cast<uint16_t*>(base) + c,
-                       make_uint4(pack16(f[0], f[1], fp16), pack16(f[2], f[3], fp16), pack16(f[4], f[5], fp16),
-                                  pack16(f[6], f[7], fp16)));
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = row_col<TPR, false>(v, t, e);
-            if (c >= C) continue;
-            if (F32) static_cast<float*>(base)[c] = f[e];
-            else static_cast<uint16_t*>(base)[c] = (uint16_t)pack16(f[e], 0.f, fp16);
+            const int c = row_col<false>(v, q.t, q.tpr, e);
+            float none;
+            if (c < q.C) {
+                if (param32) g[e] = __ldg(reinterpret_cast<const float*>(base) + c);
+                else unpack16(__ldg(reinterpret_cast<const uint16_t*>(base) + c), T16, g[e], none);
+            }
         }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pack2(g[2 * i], g[2 * i + 1]);
 }
 
-// Sum or maximum over the TPR threads of a row.  Rows of more than a warp own their CTA;
-// `slot` alternates between calls, so one barrier per reduction suffices.
-template <int TPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float (*red)[TPR / 32 > 0 ? TPR / 32 : 1], int& slot) {
+// Sum or maximum over the threads of a row: a warp's, or a CTA's.  `slot` alternates between
+// calls, so one barrier per reduction suffices.
+template <bool WARP, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float (*red)[16], int& slot) {
+    if (MAX) {  // of values that are not negative: their bits are in their order
+        v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+    } else {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, off);
-        v = MAX ? fmaxf(v, o) : v + o;
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     }
-    if (TPR > 32) {
-        const int w = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) red[slot][w] = v;
+    if (!WARP) {
+        // the slots past the CTA's warps hold zeros
+        if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = v;
         __syncthreads();
-        v = red[slot][0];
-#pragma unroll
-        for (int i = 1; i < TPR / 32; ++i) v = MAX ? fmaxf(v, red[slot][i]) : v + red[slot][i];
+        const float4* r = reinterpret_cast<const float4*>(red[slot]);
+        const float4 a = r[0], b = r[1];
+        v = MAX ? fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)))
+                : ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+        if (blockDim.x > 256) {
+            const float4 c = r[2], d = r[3];
+            const float w = MAX ? fmaxf(fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)), fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)))
+                                : ((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w));
+            v = MAX ? fmaxf(v, w) : v + w;
+        }
         slot ^= 1;
     }
     return v;
@@ -230,232 +262,354 @@ __device__ __forceinline__ float row_reduce(float v, float (*red)[TPR / 32 > 0 ?
 
 // 1 / sqrt(mean of squares + eps) of the row's values (`centre`: about their mean, which is
 // subtracted).  Columns past C hold 0 on entry and on return.
-template <int TPR, int VPT, bool VEC>
-__device__ __forceinline__ float row_statistics(float (&f)[VPT][8], bool centre, int t, int C, float eps,
-                                                float (*red)[TPR / 32 > 0 ? TPR / 32 : 1], int& slot) {
-    const float inv_c = 1.f / (float)C;
+template <bool WARP, int VPT, bool VEC>
+__device__ __forceinline__ float row_statistics(uint64_t (&f)[VPT][4], bool centre, const RowPlace& q, float inv_c,
+                                                float eps, float (*red)[16], int& slot) {
+    float a, b;
     if (centre) {
-        float s = 0.f;
+        uint64_t s = pack2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += f[v][e];
+            for (int i = 0; i < 4; ++i) s = fadd2(s, f[v][i]);
         }
-        const float mean = row_reduce<TPR, false>(s, red, slot) * inv_c;
+        unpack2(s, a, b);
+        const float mean = row_reduce<WARP, false>(a + b, red, slot) * inv_c;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
+            if (VEC) {
+                const float m = v < q.live ? -mean : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (VEC ? row_col<TPR, true>(v, t, 0) < C : row_col<TPR, false>(v, t, e) < C) f[v][e] -= mean;
+                for (int i = 0; i < 4; ++i) f[v][i] = fadd2(f[v][i], pack2(m, m));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[v][i] = fadd2(f[v][i], pack2(row_has<false>(q, v, 2 * i) ? -mean : 0.f,
+                                                   row_has<false>(q, v, 2 * i + 1) ? -mean : 0.f));
+            }
         }
     }
-    float q = 0.f;
+    uint64_t s2 = pack2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(f[v][e], f[v][e], q);
+        for (int i = 0; i < 4; ++i) s2 = ffma2(f[v][i], f[v][i], s2);
     }
-    return 1.f / sqrtf(row_reduce<TPR, false>(q, red, slot) * inv_c + eps);
+    unpack2(s2, a, b);
+    return 1.f / sqrtf(row_reduce<WARP, false>(a + b, red, slot) * inv_c + eps);
 }
 
-// X32 / H32: x and r (y and h) are fp32, else 16-bit.  One CTA of max(TPR, 128) threads per
-// max(1, 128 / TPR) rows.
-template <bool X32, bool H32, int TPR, int VPT, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) residual_norm_kernel(const RowParams p) {
-    constexpr int RPC = TPR < 128 ? 128 / TPR : 1;
-    __shared__ float red[2][TPR / 32 > 0 ? TPR / 32 : 1];
+__device__ __forceinline__ uint64_t row_mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A step of the row with one parameter: f = f a, f + a, or f + a z.
+enum RowStep : int { kStepMul, kStepAdd, kStepGate };
+template <int STEP, int T16, int VPT, bool VEC>
+__device__ __forceinline__ void row_step(uint64_t (&f)[VPT][4], const uint64_t (&z)[VPT][4], const char* base,
+                                         int param32, const RowPlace& q) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        uint64_t a[4];
+        param_load<T16, VEC>(a, base, param32, v, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (STEP == kStepMul) f[v][i] = row_mul2(f[v][i], a[i]);
+            if (STEP == kStepAdd) f[v][i] = fadd2(f[v][i], a[i]);
+            if (STEP == kStepGate) f[v][i] = ffma2(a[i], z[v][i], f[v][i]);
+        }
+    }
+}
+
+// The calls a transformer block makes have kernels of their own: in the general one
+// (kRowAny), which asks for every step as it goes, instruction fetch and issue cost more
+// than memory does (5120 channels in bf16, of the copy rate: the modulated norm 58%, with the
+// gated residual 80%; on their own 78% and 94%).
+enum RowKind : int {
+    kRowAny,
+    kRowQuant,         // codes of plain rows
+    kRowQuantHeads,    // codes of rows in head layout
+    kRowNorm,          // norm with scale and shift
+    kRowNormQuant,
+    kRowGateNorm,      // gated residual, norm with scale and shift
+    kRowGateNormQuant,
+    kRowPostGateNorm,  // post norm, gated residual, norm without them
+};
+
+// XT, HT: the types of x and r, and of y and h (as RowType).  WARP: four rows per CTA of four
+// warps; otherwise a row per CTA, and as many CTAs as are resident.  P32: parameters in fp32.
+template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32>
+__global__ void __launch_bounds__(WARP ? 128 : VPT > 4 ? 512 : 256, WARP ? 4 : VPT > 4 ? 1 : 2) residual_norm_kernel(
+    const __grid_constant__ RowParams p) {
+    __shared__ __align__(16) float red[2][16];
     int slot = 0;
-    const int t = TPR < 128 ? threadIdx.x % TPR : threadIdx.x;
-    const long long row = (long long)blockIdx.x * RPC + (TPR < 128 ? threadIdx.x / TPR : 0);
-    if (row >= p.rows) return;
-    const int b = (int)(row / p.N), n = (int)(row % p.N);
-    const int C = p.C;
-    constexpr int XW = X32 ? 4 : 2, HW = H32 ? 4 : 2;
-    char* rrow = static_cast<char*>(p.r) + (b * p.r_sb + n * p.r_sn) * XW;
-    char* hrow = static_cast<char*>(p.h) + (b * p.h_sb + n * p.h_sn) * (p.quant ? 1 : HW);
+    const int tpr = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    constexpr int rpc = WARP ? 4 : 1;
+    const uint32_t rows = (uint32_t)p.rows, N = (uint32_t)p.N, stride = gridDim.x * rpc;
+    if (!WARP) {
+        if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+        __syncthreads();
+    }
+    constexpr bool kAny = KIND == kRowAny;
+    const int param32 = kAny ? p.param32 : P32;  // a branch on it would part the loads of the chunks
+    constexpr bool kGated = KIND == kRowGateNorm || KIND == kRowGateNormQuant || KIND == kRowPostGateNorm;
+    constexpr bool kModulated = KIND == kRowNorm || KIND == kRowNormQuant || KIND == kRowGateNorm || KIND == kRowGateNormQuant;
+    const bool has_y = kAny ? p.y != nullptr : kGated;
+    const bool has_gate = kAny ? p.gate != nullptr : kGated;
+    const bool has_post = kAny ? p.post != 0 : KIND == kRowPostGateNorm;
+    const bool has_norm = kAny ? p.norm != 0 : KIND != kRowQuant && KIND != kRowQuantHeads;
+    const bool has_scale = kAny ? p.scale != nullptr : kModulated;
+    const bool has_shift = kAny ? p.shift != nullptr : kModulated;
+    const bool quant = kAny ? p.quant != 0 : KIND == kRowQuant || KIND == kRowQuantHeads || KIND == kRowNormQuant || KIND == kRowGateNormQuant;
+    const bool heads = kAny ? p.D != 0 : KIND == kRowQuantHeads;
+    constexpr int XW = XT == kRowFp32 ? 4 : 2, HW = HT == kRowFp32 ? 4 : 2;
+    const RowPlace q{t, tpr, p.C, min(VPT, max(0, (p.C / 8 - t + tpr - 1) / tpr))};
+    const float inv_c = 1.f / (float)p.C;
+    Raw8<XT, VEC> rx[VPT];
+    Raw8<HT, VEC> ry[VPT];
 
-    float f[VPT][8];
-    if (p.valid_len && n >= p.valid_len[b]) {
-        // padding: zeros out, nothing read
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[0][e] = 0.f;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            if (p.y) row_store<X32, TPR, VEC>(rrow, f[0], p.fp16, v, t, C);
-            if (p.norm && !p.quant) row_store<H32, TPR, VEC>(hrow, f[0], p.fp16, v, t, C);
+    // A row's place in the tensors.  Rows step by the grid, within a sample by adding to the
+    // addresses: finding each row anew took more instructions than a warp's channels did.
+    struct At {
+        uint32_t row, n;
+        int b, len;
+        const char *x, *y;
+        char *r, *h;
+    };
+    const int h_width = quant ? 1 : HW;
+    const long long dx = stride * p.x_sn * XW, dy = stride * p.y_sn * HW, dr = stride * p.r_sn * XW,
+                    dh = stride * p.h_sn * h_width;
+    auto seek = [&](At& a) {
+        a.b = (int)(a.row / N);
+        a.n = a.row - a.b * N;
+        a.len = p.valid_len ? p.valid_len[a.b] : (int)N;
+        a.x = static_cast<const char*>(p.x) + (a.b * p.x_sb + a.n * p.x_sn) * XW;
+        a.y = static_cast<const char*>(p.y) + (a.b * p.y_sb + a.n * p.y_sn) * HW;
+        a.r = static_cast<char*>(p.r) + (a.b * p.r_sb + a.n * p.r_sn) * XW;
+        a.h = static_cast<char*>(p.h) + (a.b * p.h_sb + a.n * p.h_sn) * h_width;
+    };
+    auto step = [&](At& a) {
+        a.row += stride;
+        a.n += stride;
+        if (a.n < N) {
+            a.x += dx;
+            a.y += dy;
+            a.r += dr;
+            a.h += dh;
+        } else if (a.row < rows) {
+            seek(a);
         }
-        if (p.quant) {
-            for (int c = 16 * t; c < p.Cq; c += 16 * TPR) *reinterpret_cast<uint4*>(hrow + c) = make_uint4(0, 0, 0, 0);
-            if (t == 0) p.h_scale[row] = 0.f;
-        }
-        return;
-    }
-
-    // every load of the row before any use
-    Raw8<X32> rx[VPT];
-    Raw8<H32> ry[VPT];
-    const char* xrow = static_cast<const char*>(p.x) + (b * p.x_sb + n * p.x_sn) * XW;
-    if (p.D == 0) {
+    };
+    // the loads of a row (padding is not read)
+    auto load = [&](const At& a) {
+        if (a.row >= rows || (int)a.n >= a.len) return;
+        if (!heads) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) row_load<X32, TPR, VEC>(rx[v], xrow, v, t, C);
-    } else if (VEC) {
+            for (int v = 0; v < VPT; ++v) row_load<XT, VEC>(rx[v], a.x, v, q);
+        } else if (VEC) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int c = row_col<TPR, true>(v, t, 0), hd = c / p.D;
-            // the head's row, moved back so that column c of it is channel c % D
-            row_load<X32, TPR, VEC>(rx[v], xrow + (hd * p.x_sh - (long long)hd * p.D) * XW, v, t, C);
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            Raw8<X32>& raw = rx[v];
-            uint32_t u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = row_col<TPR, false>(v, t, e);
-                u[e] = 0;
-                if (c < C) {
-                    const char* q = xrow + ((c / p.D) * p.x_sh + c % p.D) * XW;
-                    u[e] = X32 ? *reinterpret_cast<const uint32_t*>(q) : *reinterpret_cast<const uint16_t*>(q);
-                }
-            }
-            if (X32) {
-                raw.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-                raw.w[X32 ? 1 : 0] = make_uint4(u[4], u[5], u[6], u[7]);
-            } else {
-                raw.w[0] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
-            }
-        }
-    }
-    if (p.y) {
-        const char* yrow = static_cast<const char*>(p.y) + (b * p.y_sb + n * p.y_sn) * HW;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) row_load<H32, TPR, VEC>(ry[v], yrow, v, t, C);
-    }
-    // the row's modulation row
-    int g = b;
-    if (p.index) {
-        g = p.index[(long long)b * p.N + n];
-        if (g < 0 || g >= p.G) {
-            if (t == 0) raise_device_error(kErrBadRouting);
-            g = 0;
-        }
-    }
-    const long long goff = (long long)g * C * (p.param32 ? 4 : 2);
-
-    if (p.y) {
-        float z[VPT][8];
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            raw_to_float<H32>(ry[v], p.fp16, z[v]);
-            if (VEC && row_col<TPR, true>(v, t, 0) >= C) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[v][e] = 0.f;
-            }
-        }
-        float inv = 1.f;
-        if (p.post) inv = row_statistics<TPR, VPT, VEC>(z, p.post == kNormLayer, t, C, p.eps, red, slot);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            float a[8];
-            if (p.post) {
-                if (p.post_weight) {
-                    param_load<TPR, VEC>(a, p.post_weight, p.param32, p.fp16, v, t, C);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z[v][e] *= inv * a[e];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z[v][e] *= inv;
-                }
-            }
-            raw_to_float<X32>(rx[v], p.fp16, f[v]);
-            if (p.gate) {
-                param_load<TPR, VEC>(a, static_cast<const char*>(p.gate) + goff, p.param32, p.fp16, v, t, C);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] = fmaf(a[e], z[v][e], f[v][e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] += z[v][e];
-            }
-            row_store<X32, TPR, VEC>(rrow, f[v], p.fp16, v, t, C);
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) raw_to_float<X32>(rx[v], p.fp16, f[v]);
-    }
-    if (!p.norm && !p.quant) return;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        if (VEC && row_col<TPR, true>(v, t, 0) >= C) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[v][e] = 0.f;
-        }
-    }
-
-    if (p.norm) {
-        const float inv = row_statistics<TPR, VPT, VEC>(f, p.norm == kNormLayer, t, C, p.eps, red, slot);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            float a[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[v][e] *= inv;
-            if (p.weight) {
-                param_load<TPR, VEC>(a, p.weight, p.param32, p.fp16, v, t, C);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] *= a[e];
-            }
-            if (p.bias) {
-                param_load<TPR, VEC>(a, p.bias, p.param32, p.fp16, v, t, C);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] += a[e];
-            }
-            if (p.scale) {
-                param_load<TPR, VEC>(a, static_cast<const char*>(p.scale) + goff, p.param32, p.fp16, v, t, C);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] = fmaf(f[v][e], a[e], f[v][e]);
-            }
-            if (p.shift) {
-                param_load<TPR, VEC>(a, static_cast<const char*>(p.shift) + goff, p.param32, p.fp16, v, t, C);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] += a[e];
-            }
-            if (!p.quant) row_store<H32, TPR, VEC>(hrow, f[v], p.fp16, v, t, C);
-        }
-    }
-    if (!p.quant) return;
-
-    // Columns past C hold 0 here or are masked below, so they change no maximum.
-    float top = 0.f;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[v][e]));
-    }
-    top = row_reduce<TPR, true>(top, red, slot);
-    // below 2^-100 the reciprocal step would leave fp32's range: such a row counts as zero
-    const bool zero = !(top >= 7.888609052210118e-31f);
-    const float inv = zero ? 0.f : __fdiv_rn(127.f, top);
-    if (t == 0) p.h_scale[row] = zero ? 0.f : __fdiv_rn(top, 127.f);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        int q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = __float2int_rn(__fmul_rn(f[v][e], inv));
-        if (VEC) {
-            const int c = row_col<TPR, true>(v, t, 0);
-            if (c < p.Cq) {
-                uint2 w;
-                w.x = (q[0] & 255) | (q[1] & 255) << 8 | (q[2] & 255) << 16 | (uint32_t)q[3] << 24;
-                w.y = (q[4] & 255) | (q[5] & 255) << 8 | (q[6] & 255) << 16 | (uint32_t)q[7] << 24;
-                *reinterpret_cast<uint2*>(hrow + c) = w;
+            for (int v = 0; v < VPT; ++v) {
+                const int hd = row_col<true>(v, t, tpr, 0) / p.D;
+                // the head's row, moved back so that column c of it is channel c % D
+                row_load<XT, VEC>(rx[v], a.x + hd * (p.x_sh - p.D) * XW, v, q);
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = row_col<TPR, false>(v, t, e);
-                if (c < p.Cq) hrow[c] = (char)q[e];
+            for (int v = 0; v < VPT; ++v) {
+                uint32_t u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = row_col<false>(v, t, tpr, e);
+                    u[e] = 0;
+                    if (c < p.C) {
+                        const char* at = a.x + ((c / p.D) * p.x_sh + c % p.D) * XW;
+                        u[e] = XW == 4 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+                    }
+                }
+                rx[v].w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                rx[v].w[Raw8<XT, VEC>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
             }
         }
+        if (has_y) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) row_load<HT, VEC>(ry[v], a.y, v, q);
+        }
+    };
+
+    constexpr bool kAhead = VEC && VPT <= 4;  // registers for a second row
+    At next;
+    next.row = blockIdx.x * rpc + (WARP ? threadIdx.x >> 5 : 0);
+    if (next.row >= rows) return;
+    seek(next);
+    load(next);
+    while (next.row < rows) {
+        const At at = next;
+        step(next);
+        uint64_t f[VPT][4];
+        if ((int)at.n >= at.len) {
+            // padding: zeros out, nothing read
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[0][i] = 0;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                if (has_y) row_store<XT, VEC>(at.r, f[0], v, q);
+                if (has_norm && !quant) row_store<HT, VEC>(at.h, f[0], v, q);
+            }
+            if (quant) {
+                for (int c = 16 * t; c < p.Cq; c += 16 * tpr) *reinterpret_cast<uint4*>(at.h + c) = make_uint4(0, 0, 0, 0);
+                if (t == 0) p.h_scale[at.row] = 0.f;
+            }
+            load(next);
+            continue;
+        }
+
+        // the row's modulation row
+        int g = at.b;
+        if (p.index) {
+            g = p.index[at.row];
+            if (g < 0 || g >= p.G) {
+                if (t == 0) raise_device_error(kErrBadRouting);
+                g = 0;
+            }
+        }
+        const long long goff = (long long)g * p.C * (param32 ? 4 : 2);
+
+        if (has_y) {
+            uint64_t z[VPT][4];
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) row_values<HT, VEC>(ry[v], z[v]);
+            float inv = 1.f;
+            if (has_post) inv = row_statistics<WARP, VPT, VEC>(z, p.post == kNormLayer, q, inv_c, p.eps, red, slot);
+            if (has_post) {
+                const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[v][i] = row_mul2(z[v][i], inv2);
+                }
+                if (p.post_weight) row_step<kStepMul, HT, VPT, VEC>(z, z, static_cast<const char*>(p.post_weight), param32, q);
+            }
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) row_values<XT, VEC>(rx[v], f[v]);
+            if (has_gate) {
+                row_step<kStepGate, HT, VPT, VEC>(f, z, static_cast<const char*>(p.gate) + goff, param32, q);
+            } else {
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[v][i] = fadd2(f[v][i], z[v][i]);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) row_store<XT, VEC>(at.r, f[v], v, q);
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) row_values<XT, VEC>(rx[v], f[v]);
+        }
+
+        // the next row's loads run under this one's statistics and stores
+        if (kAhead) load(next);
+
+        if (has_norm) {
+            const float inv = row_statistics<WARP, VPT, VEC>(f, p.norm == kNormLayer, q, inv_c, p.eps, red, slot);
+            const uint64_t inv2 = pack2(inv, inv);
+            uint64_t none[VPT][4];
+            if (p.weight) row_step<kStepMul, HT, VPT, VEC>(f, none, static_cast<const char*>(p.weight), param32, q);
+            if (!p.bias && has_scale) {
+                // f inv (1 + scale) + shift in two steps: f (inv + inv scale) + shift
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) {
+                    uint64_t a[4];
+                    param_load<HT, VEC>(a, static_cast<const char*>(p.scale) + goff, param32, v, q);
+                    if (has_shift) {
+                        uint64_t s[4];
+                        param_load<HT, VEC>(s, static_cast<const char*>(p.shift) + goff, param32, v, q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[v][i] = ffma2(f[v][i], ffma2(a[i], inv2, inv2), s[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[v][i] = row_mul2(f[v][i], ffma2(a[i], inv2, inv2));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[v][i] = row_mul2(f[v][i], inv2);
+                }
+                if (p.bias) row_step<kStepAdd, HT, VPT, VEC>(f, none, static_cast<const char*>(p.bias), param32, q);
+                if (has_scale) {
+#pragma unroll
+                    for (int v = 0; v < VPT; ++v) {
+                        uint64_t a[4];
+                        param_load<HT, VEC>(a, static_cast<const char*>(p.scale) + goff, param32, v, q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[v][i] = ffma2(f[v][i], a[i], f[v][i]);
+                    }
+                }
+                if (has_shift)
+                    row_step<kStepAdd, HT, VPT, VEC>(f, none, static_cast<const char*>(p.shift) + goff, param32, q);
+            }
+            if (!quant) {
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) row_store<HT, VEC>(at.h, f[v], v, q);
+            }
+        }
+        if (!quant) {
+            if (!kAhead) load(next);
+            continue;
+        }
+
+        // columns past C hold 0
+        float top = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                unpack2(f[v][i], lo, hi);
+                asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(lo), "f"(hi));
+            }
+        }
+        top = row_reduce<WARP, true>(top, red, slot);
+        // below 2^-100 the reciprocal step would leave fp32's range: such a row counts as zero
+        const bool zero = !(top >= 7.888609052210118e-31f);
+        const float inv = zero ? 0.f : __fdiv_rn(127.f, top);
+        if (t == 0) p.h_scale[at.row] = zero ? 0.f : __fdiv_rn(top, 127.f);
+        // Adding 1.5 * 2^23 to a product of at most 127 rounds it to the nearest integer, ties to
+        // even, and leaves that integer in the low byte.  Both steps round by definition: packed,
+        // the compiler makes one fused step of them, which decides some ties otherwise.
+        constexpr float kMagic = 12582912.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            uint32_t code[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                unpack2(f[v][i], lo, hi);
+                code[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(lo, inv), kMagic));
+                code[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(hi, inv), kMagic));
+            }
+            if (VEC) {
+                const int c = row_col<true>(v, t, tpr, 0);
+                if (c < p.Cq) {
+                    uint2 w;
+                    w.x = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
+                    w.y = __byte_perm(__byte_perm(code[4], code[5], 0x0040), __byte_perm(code[6], code[7], 0x0040), 0x5410);
+                    *reinterpret_cast<uint2*>(at.h + c) = w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = row_col<false>(v, t, tpr, e);
+                    if (c < p.Cq) at.h[c] = (char)code[e];
+                }
+            }
+        }
+        if (!kAhead) load(next);
     }
 }
 

@@ -49,11 +49,29 @@ __device__ __forceinline__ void rotary_sincos(const RotaryParams& p, const int32
 
 // Eight consecutive values, 16-byte accesses.
 template <bool F32>
-__device__ __forceinline__ Raw8<F32> rotary_load(const char* q) {
-    Raw8<F32> r;
+struct Raw8Words {
+    uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8Words<F32> rotary_load(const char* q) {
+    Raw8Words<F32> r;
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) r.w[i] = ldg_stream(q + 16 * i);
     return r;
+}
+template <bool F32>
+__device__ __forceinline__ void rotary_values(const Raw8Words<F32>& raw, int fp16, float (&f)[8]) {
+    const uint4 a = raw.w[0], b = raw.w[F32 ? 1 : 0];
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        if (F32) {
+            f[e] = __uint_as_float(u[e]);
+            f[e + 1] = __uint_as_float(u[e + 1]);
+        } else {
+            unpack16(u[e / 2], fp16, f[e], f[e + 1]);
+        }
+    }
 }
 template <bool F32>
 __device__ __forceinline__ void rotary_store(char* q, const float (&f)[8], int fp16) {
@@ -94,7 +112,7 @@ __global__ void __launch_bounds__(256) rotary_vec_kernel(const __grid_constant__
         for (int e = 0; e < 8; ++e) rotary_sincos(p, pos, 8 * j + e, s[e], c[e]);
     }
     for (int h = h0; h < h1; h += U) {
-        Raw8<F32> ra[U], rb[U];
+        Raw8Words<F32> ra[U], rb[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (h + i < h1) {
@@ -106,8 +124,8 @@ __global__ void __launch_bounds__(256) rotary_vec_kernel(const __grid_constant__
         for (int i = 0; i < U; ++i) {
             if (h + i >= h1) break;
             float a[8], d[8];
-            raw_to_float<F32>(ra[i], p.fp16, a);
-            raw_to_float<F32>(rb[i], p.fp16, d);
+            rotary_values<F32>(ra[i], p.fp16, a);
+            rotary_values<F32>(rb[i], p.fp16, d);
             if (turned && p.half) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {

@@ -803,39 +803,68 @@ bool none_negative(const int64_t* s, int n) {
     return true;
 }
 
-template <bool X32, bool H32, int TPR, int VPT, bool VEC>
-sba_status launch_rows(const sba::RowParams& p, cudaStream_t s) {
-    constexpr int threads = TPR < 128 ? 128 : TPR, rpc = TPR < 128 ? 128 / TPR : 1;
-    sba::residual_norm_kernel<X32, H32, TPR, VPT, VEC><<<(unsigned)((p.rows + rpc - 1) / rpc), threads, 0, s>>>(p);
+template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32 = true>
+sba_status launch_rows(const sba::RowParams& p, int chunks, cudaStream_t s) {
+    const auto kernel = sba::residual_norm_kernel<XT, HT, WARP, VPT, VEC, KIND, P32>;
+    const int threads = WARP ? 128 : (chunks + 32 * VPT - 1) / (32 * VPT) * 32;
+    int dev = 0, sms = 0, resident = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, 0) != cudaSuccess)
+        return SBA_ERR_CUDA;
+    const long long ctas = WARP ? (p.rows + 3) / 4 : p.rows, most = (long long)sms * resident;
+    kernel<<<(unsigned)(ctas < most ? ctas : most), threads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
 }
 
-// The threads and chunks per row: the fewest registers that hold the row.
-template <bool X32, bool H32>
+// Which of the kernels with fixed steps a call is.
+int row_kind(const sba::RowParams& p) {
+    if (!p.norm) return p.y ? sba::kRowAny : p.D ? sba::kRowQuantHeads : sba::kRowQuant;
+    const bool modulated = p.scale && p.shift && !p.bias;
+    if (!p.y && modulated) return p.quant ? sba::kRowNormQuant : sba::kRowNorm;
+    if (p.y && p.gate && !p.post && modulated) return p.quant ? sba::kRowGateNormQuant : sba::kRowGateNorm;
+    if (p.y && p.gate && p.post && !p.scale && !p.shift && !p.quant) return sba::kRowPostGateNorm;
+    return sba::kRowAny;
+}
+
+template <int XT, int HT, bool P32>
+sba_status run_kind(const sba::RowParams& p, int chunks, cudaStream_t s) {
+    switch (row_kind(p)) {
+        case sba::kRowNorm: return launch_rows<XT, HT, false, 4, true, sba::kRowNorm, P32>(p, chunks, s);
+        case sba::kRowNormQuant: return launch_rows<XT, HT, false, 4, true, sba::kRowNormQuant, P32>(p, chunks, s);
+        case sba::kRowGateNorm: return launch_rows<XT, HT, false, 4, true, sba::kRowGateNorm, P32>(p, chunks, s);
+        case sba::kRowGateNormQuant: return launch_rows<XT, HT, false, 4, true, sba::kRowGateNormQuant, P32>(p, chunks, s);
+        case sba::kRowPostGateNorm: return launch_rows<XT, HT, false, 4, true, sba::kRowPostGateNorm, P32>(p, chunks, s);
+    }
+    return launch_rows<XT, HT, false, 4, true, sba::kRowAny>(p, chunks, s);
+}
+
+// The warps of a row and the chunks of each thread.
+template <int XT, int HT>
 sba_status run_rows(const sba::RowParams& p, bool vec, cudaStream_t s) {
     const int chunks = p.quant ? p.Cq / 8 : (p.C + 7) / 8;
-    if (vec) {
-        if (chunks <= 32) return launch_rows<X32, H32, 32, 1, true>(p, s);
-        if (chunks <= 64) return launch_rows<X32, H32, 32, 2, true>(p, s);
-        if (chunks <= 128) return launch_rows<X32, H32, 32, 4, true>(p, s);
-        if (chunks <= 256) return launch_rows<X32, H32, 128, 2, true>(p, s);
-        if (chunks <= 384) return launch_rows<X32, H32, 128, 3, true>(p, s);
-        if (chunks <= 512) return launch_rows<X32, H32, 128, 4, true>(p, s);
-        if (chunks <= 640) return launch_rows<X32, H32, 128, 5, true>(p, s);
-        if (chunks <= 768) return launch_rows<X32, H32, 128, 6, true>(p, s);
-        if (chunks <= 1024) return launch_rows<X32, H32, 256, 4, true>(p, s);
-        if (chunks <= 2048) return launch_rows<X32, H32, 512, 4, true>(p, s);
-        return launch_rows<X32, H32, 512, 8, true>(p, s);
+    if (!vec) {
+        if (chunks <= 128) return launch_rows<XT, HT, true, 4, false, sba::kRowAny>(p, chunks, s);
+        return launch_rows<XT, HT, false, 8, false, sba::kRowAny>(p, chunks, s);
     }
-    if (chunks <= 128) return launch_rows<X32, H32, 32, 4, false>(p, s);
-    if (chunks <= 1024) return launch_rows<X32, H32, 256, 4, false>(p, s);
-    return launch_rows<X32, H32, 512, 8, false>(p, s);
+    if (chunks <= 32) return launch_rows<XT, HT, true, 1, true, sba::kRowAny>(p, chunks, s);
+    if (chunks <= 128) return launch_rows<XT, HT, true, 4, true, sba::kRowAny>(p, chunks, s);
+    if (chunks > 1024) return launch_rows<XT, HT, false, 8, true, sba::kRowAny>(p, chunks, s);
+    if constexpr (XT == HT) {
+        if (row_kind(p) == sba::kRowQuant) return launch_rows<XT, HT, false, 4, true, sba::kRowQuant>(p, chunks, s);
+        if (row_kind(p) == sba::kRowQuantHeads)
+            return launch_rows<XT, HT, false, 4, true, sba::kRowQuantHeads>(p, chunks, s);
+    }
+    if constexpr (HT != sba::kRowFp32) return p.param32 ? run_kind<XT, HT, true>(p, chunks, s) : run_kind<XT, HT, false>(p, chunks, s);
+    return launch_rows<XT, HT, false, 4, true, sba::kRowAny>(p, chunks, s);
 }
 
 sba_status dispatch_rows(const sba::RowParams& p, int x_dtype, int dtype, bool vec, cudaStream_t s) {
-    if (x_dtype != SBA_DTYPE_FP32) return run_rows<false, false>(p, vec, s);
-    if (dtype != SBA_DTYPE_FP32) return run_rows<true, false>(p, vec, s);
-    return run_rows<true, true>(p, vec, s);
+    if (x_dtype == SBA_DTYPE_BF16) return run_rows<0, 0>(p, vec, s);
+    if (x_dtype == SBA_DTYPE_FP16) return run_rows<1, 1>(p, vec, s);
+    if (dtype == SBA_DTYPE_BF16) return run_rows<2, 0>(p, vec, s);
+    if (dtype == SBA_DTYPE_FP16) return run_rows<2, 1>(p, vec, s);
+    return run_rows<2, 2>(p, vec, s);
 }
 
 // Row-major [rows][K] 8-bit codes as a 2-D tensor; box = 128 codes x box_rows, 128-byte swizzle.
@@ -850,6 +879,54 @@ bool make_map_codes(CUtensorMap* map, const void* base, long long rows, int K, i
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+// How a product runs: the pair kernel with tiles of 256 x bn (splits = 0), or the split
+// kernel with tiles of 128 x bn and K in `splits` parts.
+struct LinearPlan {
+    int bn, splits;
+};
+
+// The plan of least estimated time, in microseconds.  The estimates follow what bounds each form:
+// K steps of a tile (which are latency and issue up to about 128 columns and tensor work above), the
+// epilogue that the next tile's steps hide or do not, the operands' way from L2, W's way from
+// HBM; for the split kernel also the staged sums and the CTAs past one per SM, whose start
+// costs more in clusters.  Constants fitted to 84 sizes (2 to 512 rows, 320 to 24576
+// channels, 512 to 16384 codes) with every plan timed at each: the chosen plan took 1.5%
+// longer than the fastest on average, 16% at worst.  Per size, splitting against the pair kernel:
+// 2 x 24576 x 4096 codes 15.4 against 33 us, 128 x 320 x 16384 9.1 against 17 us; the
+// other way at 128 x 5120 x 512 10.0 against 7.4 us and 512 x 5120 x 4096 22.7 against 14.6 us.
+LinearPlan plan_linear(long long M, long long N, long long K, int sms) {
+    const double ks = (double)((K + 127) / 128), hbm = (double)N * K / 6.5e6;
+    LinearPlan best{256, 0};
+    double least = 1e300;
+    for (int bn = 64; bn <= 256; bn += 64) {
+        const double tiles = (double)((M + 255) / 256) * (double)((N + bn - 1) / bn);
+        const double waves = std::ceil(tiles / (sms / 2)), step = 0.021 + 0.0018 * bn, out = 3.0 + 0.0091 * bn;
+        const double loop = std::fmax(std::fmax(ks * step + out + (waves - 1) * std::fmax(ks * step, out),
+                                                tiles * ks * (256 + bn) * 128 / 14e6 + out), hbm);
+        if (1.7 + loop < least) {
+            least = 1.7 + loop;
+            best = LinearPlan{bn, 0};
+        }
+    }
+    const double box = M < 128 ? (double)((M + 7) / 8 * 8) : 128.0;
+    for (int bn = 64; bn <= 128; bn += 64) {
+        for (int splits = 1; splits <= 8 && (splits == 1 || ks >= 2 * splits); splits *= 2) {
+            const double ctas = (double)((M + 127) / 128) * (double)((N + bn - 1) / bn) * splits, per = ctas / sms;
+            const double part = std::ceil(ks / splits);
+            const double sums = box * bn * (0.00062 / splits + (splits > 1 ? 0.0001 : 0.0));
+            const double more = per > 1 ? (per - 1) * ((splits > 1 ? 3.8 : 0.13) + 0.5 * sums) : 0.0;
+            const double loop = std::fmax(std::fmax(part * (0.072 + 0.001 * bn) * std::fmax(1.0, 0.59 * per),
+                                                    ctas * part * (bn + box) * 128 / 7.2e6), hbm);
+            const double est = 3.7 + (splits > 1 ? 0.95 : 0.0) + sums + more + loop;
+            if (est < least) {
+                least = est;
+                best = LinearPlan{bn, splits};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -895,13 +972,12 @@ extern "C" sba_status sba_residual_norm(const void* x, const void* y, void* x_ou
     p.norm = norm; p.post = post_norm; p.quant = out_scale != nullptr;
     p.Cq = (C + 15) / 16 * 16;
     if (p.quant && (p.h_sb % 16 || p.h_sn % 16)) return SBA_ERR_ALIGNMENT;
-    p.fp16 = dtype == SBA_DTYPE_FP16;
     p.param32 = param_dtype == SBA_DTYPE_FP32;
     p.eps = eps;
     const bool vec = C % 8 == 0 && rows16(x, strides, 2, xw) && (!y || (rows16(y, strides + 2, 2, hw) &&
                      rows16(x_out, strides + 4, 2, xw))) && (!norm || p.quant || rows16(out, strides + 6, 2, hw)) &&
-                     aligned16(weight) && aligned16(bias) && aligned16(post_weight) && aligned16(gate) &&
-                     aligned16(scale) && aligned16(shift);
+                     aligned_to(weight, 8 * pw) && aligned_to(bias, 8 * pw) && aligned_to(post_weight, 8 * pw) &&
+                     aligned_to(gate, 8 * pw) && aligned_to(scale, 8 * pw) && aligned_to(shift, 8 * pw);
     return dispatch_rows(p, x_dtype, dtype, vec, static_cast<cudaStream_t>(stream));
 }
 
@@ -924,7 +1000,6 @@ extern "C" sba_status sba_token_quantize(const void* x, int dtype, int B, int H,
     p.h_sb = (long long)N * p.Cq;
     p.rows = (long long)B * N;
     p.quant = 1;
-    p.fp16 = dtype == SBA_DTYPE_FP16;
     const bool vec = D % 8 == 0 && rows16(x, strides, 3, w);
     return dispatch_rows(p, dtype, dtype, vec, static_cast<cudaStream_t>(stream));
 }
@@ -971,11 +1046,15 @@ extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, con
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
         return SBA_ERR_CUDA;
     CUtensorMap ta, tw;
-    const long long pair_tiles = ((p.M + 255ll) / 256) * ((p.N + 255ll) / 256);
-    if (pair_tiles > 0x3fffffffll) return SBA_ERR_UNSUPPORTED;
-    if (p.M > 128 && pair_tiles >= sms / 4) {
+    const LinearPlan plan = plan_linear(p.M, p.N, K, sms);
+    p.bn = plan.bn;
+    const long long tiles_n = (p.N + p.bn - 1ll) / p.bn;
+    if (plan.splits == 0) {
+        const long long pair_tiles = (p.M + 255ll) / 256 * tiles_n;
+        if (pair_tiles > 0x3fffffffll) return SBA_ERR_UNSUPPORTED;
         using SM = sba::PairSmem;
-        if (!make_map_codes(&ta, a, p.M, K, 128) || !make_map_codes(&tw, w, M, K, 128)) return SBA_ERR_CUDA;
+        p.stages = SM::stages(p.bn);
+        if (!make_map_codes(&ta, a, p.M, K, 128) || !make_map_codes(&tw, w, M, K, p.bn / 2)) return SBA_ERR_CUDA;
         if (cudaFuncSetAttribute(sba::int8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) !=
             cudaSuccess)
             return SBA_ERR_CUDA;
@@ -985,19 +1064,22 @@ extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, con
     }
     using SM = sba::SplitSmem;
     p.box_rows = p.M < 128 ? (p.M + 7) / 8 * 8 : 128;
-    if (!make_map_codes(&ta, a, p.M, K, p.box_rows) || !make_map_codes(&tw, w, M, K, SM::kBN)) return SBA_ERR_CUDA;
-    if (cudaFuncSetAttribute(sba::int8_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) !=
-        cudaSuccess)
+    const int splits = plan.splits;
+    const long long tiles_m = (p.M + 127ll) / 128, ctas = tiles_n * tiles_m * splits;
+    if (tiles_m > 65535 || tiles_n * splits > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
+    // CTAs share an SM's memory, up to three where there are that many
+    const int per_sm = ctas > 2 * sms ? 3 : ctas > sms ? 2 : 1;
+    p.stages = sba::kMaxStages;
+    while (p.stages > 2 && (SM::alloc(p.bn, p.box_rows, p.stages) + 1024) * per_sm > 227 * 1024) --p.stages;
+    const int smem = SM::alloc(p.bn, p.box_rows, p.stages);
+    if (!make_map_codes(&ta, a, p.M, K, p.box_rows) || !make_map_codes(&tw, w, M, K, p.bn)) return SBA_ERR_CUDA;
+    if (cudaFuncSetAttribute(sba::int8_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return SBA_ERR_CUDA;
-    const int tiles_n = (p.N + SM::kBN - 1) / SM::kBN, tiles_m = (p.M + 127) / 128;
-    const int ksteps = (K + 127) / 128;
-    int splits = 1;
-    while (splits < 8 && 2 * splits * 4 <= ksteps && (long long)tiles_n * tiles_m * splits < 2 * sms) splits *= 2;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)(tiles_n * splits), (unsigned)tiles_m);
     cfg.blockDim = dim3(sba::kSplitThreads);
-    cfg.dynamicSmemBytes = SM::kAlloc;
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

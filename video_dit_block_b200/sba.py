@@ -7,8 +7,8 @@ CUDA device, the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -125,6 +125,11 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw(t):
+    """The address of an optional tensor, as the plain integer that ctypes takes for a void *."""
+    return None if t is None else t.data_ptr()
 
 
 def _check(code, what):
@@ -478,43 +483,51 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NORMS = {None: 0, "layer": 1, "rms": 2}
 _ACTS = {None: 0, "gelu_tanh": 1, "silu": 2}
 _LAYOUTS = {"interleaved": 0, "half": 1}
-_HERE = contextlib.nullcontext()
+_Strides3, _Strides5, _Strides6, _Strides8 = (ctypes.c_int64 * n for n in (3, 5, 6, 8))
 
 
-def _place(t, stream):
-    """The context of a call on t's device: its allocations and launch on `stream`, or on
-    the device's current stream."""
-    if not t.is_cuda:
+def _place(device, stream):
+    """The context of a call on GPU `device` (its index): allocations and launch on `stream`, or
+    on the device's current stream.  None when that is where the caller is already."""
+    if device < 0:
         raise ValueError("expected CUDA tensors")
     if stream is None:
-        if t.device.index == torch.cuda.current_device():
-            return _HERE
-        return torch.cuda.device(t.device)
-    if stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return None if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
     return torch.cuda.stream(stream)
 
 
-def _values(t, name, shape, device, dtypes):
-    """Check an optional tensor: shape, device, type, and contiguous unless `shape` is None."""
-    if t is None:
-        return
-    if t.device != device or t.dtype not in dtypes or (shape is not None and (
-            tuple(t.shape) != tuple(shape) or not t.is_contiguous())):
-        want = "" if shape is None else f" contiguous {tuple(shape)}"
-        raise ValueError(f"{name}: expected a{want} tensor on {device} of {' or '.join(str(d) for d in dtypes)}, got "
+def _on_device(call):
+    """Runs an operator where its first tensor lives, on the `stream` that it is given."""
+    @functools.wraps(call)
+    def placed(x, *args, stream=None, **kwargs):
+        where = _place(x.get_device(), stream)
+        if where is None:
+            return call(x, *args, **kwargs)
+        with where:
+            return call(x, *args, **kwargs)
+    return placed
+
+
+def _values(t, name, shape, device, dtype):
+    """Check an optional tensor: shape, device, type, contiguous."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} tensor of {dtype} on cuda:{device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 def _rows(t, name, shape, device, dtype, written=False):
     """Check rows at any strides: the last dimension contiguous, and no two elements of a
     written tensor in one place."""
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
+    if t.get_device() != device or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{device}, got {tuple(t.shape)} {t.dtype} on "
                          f"{t.device}")
+    if t.is_contiguous():
+        return
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if written and not t.is_contiguous():
+    if written:
         reach = 0
         for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
             if stride <= reach:
@@ -522,39 +535,43 @@ def _rows(t, name, shape, device, dtype, written=False):
             reach += stride * (size - 1)
 
 
-def _param_dtype(params, dtype, device, shapes):
-    """The one type of the parameters given (name, tensor) -- fp32 or `dtype` -- as a code."""
-    given = [(n, t) for n, t in params if t is not None]
-    if not given:
-        return 2
-    kind = given[0][1].dtype
-    if kind != torch.float32 and kind != dtype:
-        raise ValueError(f"{given[0][0]}: expected torch.float32 or {dtype}, got {kind}")
-    for n, t in given:
-        _values(t, n, shapes[n], device, (kind,))
-    return _DTYPES[kind]
+def _params(params, shape, dtype, device, kind=None):
+    """Check parameters (name, tensor or None) of one shape and one type, fp32 or `dtype`: that
+    of `kind`, where earlier ones have set it.  Returns the type, or None as it came."""
+    for name, t in params:
+        if t is None:
+            continue
+        if kind is None:
+            kind = t.dtype
+            if kind != torch.float32 and kind != dtype:
+                raise ValueError(f"{name}: expected torch.float32 or {dtype}, got {kind}")
+        _values(t, name, shape, device, kind)
+    return kind
 
 
-def _index_rows(index, tables, rows, B, device):
-    """Rows of the modulation tables: (their count, the index or None).  Without an index
-    sample b takes row b."""
-    sizes = {t.shape[0] if t.dim() == 2 else -1 for t in tables if t is not None}
-    if len(sizes) > 1 or -1 in sizes:
-        raise ValueError("gate, scale and shift must be [G, C] with one G")
-    G = sizes.pop() if sizes else 0
-    if index is None:
-        if G and G != B:
-            raise ValueError(f"{G} modulation rows for {B} samples, and no index")
-        return G
-    _values(index, "index", rows, device, (torch.int32,))
-    if not G:
-        raise ValueError("an index, and nothing that it selects from")
-    return G
+def _tables(tables, C, index, rows, dtype, device, kind=None):
+    """Check modulation tables [G, C] (name, tensor or None) and the index of their rows;
+    without an index sample b takes row b, so G = B.  Returns (G, the parameters' type)."""
+    G = 0
+    for _, t in tables:
+        if t is not None:
+            G = t.shape[0] if t.dim() == 2 else 0
+            if not G:
+                raise ValueError("gate, scale and shift must be [G, C], G at least 1")
+            break
+    if index is not None:
+        if not G:
+            raise ValueError("an index, and nothing that it selects from")
+        _values(index, "index", rows, device, torch.int32)
+    elif G and G != (rows[0] if len(rows) == 2 else 1):
+        raise ValueError(f"{G} modulation rows for a batch of {rows[0] if len(rows) == 2 else 1}, and no index")
+    return G, _params(tables, (G, C), dtype, device, kind)
 
 
+@_on_device
 def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, scale=None, shift=None, index=None,
                   post_norm=None, post_weight=None, valid_len=None, eps: float = 1e-6, quantize: bool = False,
-                  out_dtype=None, x_out=None, out=None, out_scale=None, stream=None):
+                  out_dtype=None, x_out=None, out=None, out_scale=None):
     """The gated residual of a block's output y, and the modulated norm of the new residual
     stream, in one pass (see include/sba.h).
 
@@ -571,92 +588,102 @@ def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, sc
     quantize=True returns (r, codes, scales) for int8_linear: int8 [B, N, C rounded up to
     16] and fp32 [B, N].  h has y's type (out_dtype without a y, x's by default).  x_out
     may be x, out may be y."""
-    with _place(x, stream):
-        if x.dim() != 3 or x.dtype not in _DTYPES:
-            raise ValueError("x: expected [B, N, C] in bf16, fp16 or fp32")
-        B, N, C = x.shape
-        dev = x.device
-        dtype = y.dtype if y is not None else (out_dtype or x.dtype)
-        if dtype not in _DTYPES or (dtype != x.dtype and x.dtype != torch.float32) or (
-                out_dtype is not None and out_dtype != dtype):
-            raise ValueError(f"x of {x.dtype}, y of {None if y is None else y.dtype}, out_dtype {out_dtype}: h has y's "
-                             "type, and that is x's or, next to an fp32 x, 16-bit")
-        if norm not in _NORMS or post_norm not in _NORMS:
-            raise ValueError(f"norm {norm!r}, post_norm {post_norm!r}: each one of {sorted(map(str, _NORMS))}")
-        if norm is None and (quantize or y is None):
-            raise ValueError("norm=None needs a y, and gives nothing to quantize")
-        _rows(x, "x", (B, N, C), dev, x.dtype)
-        shapes = {"weight": (C,), "bias": (C,), "post_weight": (C,)}
-        G = _index_rows(index, (gate, scale, shift), (B, N), B, dev)
-        shapes.update(gate=(G, C), scale=(G, C), shift=(G, C))
-        ptype = _param_dtype((("weight", weight), ("bias", bias), ("post_weight", post_weight), ("gate", gate),
-                              ("scale", scale), ("shift", shift)), dtype, dev, shapes)
-        _values(valid_len, "valid_len", (B,), dev, (torch.int32,))
-        strides = [x.stride(0), x.stride(1), 0, 0, 0, 0, 0, 0]
-        if y is not None:
-            _rows(y, "y", (B, N, C), dev, dtype)
-            if x_out is None:
-                x_out = torch.empty((B, N, C), dtype=x.dtype, device=dev)
-            _rows(x_out, "x_out", (B, N, C), dev, x.dtype, written=True)
-            strides[2:6] = y.stride(0), y.stride(1), x_out.stride(0), x_out.stride(1)
-        elif x_out is not None:
-            raise ValueError("x_out without a y: the residual stream does not change")
-        if norm is not None:
-            shape, kind = ((B, N, -(-C // 16) * 16), torch.int8) if quantize else ((B, N, C), dtype)
-            if out is None:
-                out = torch.empty(shape, dtype=kind, device=dev)
+    shape, dev, xtype = x.shape, x.get_device(), x.dtype
+    if len(shape) != 3 or xtype not in _DTYPES:
+        raise ValueError("x: expected [B, N, C] in bf16, fp16 or fp32")
+    B, N, C = shape
+    dtype = y.dtype if y is not None else (out_dtype or xtype)
+    if dtype not in _DTYPES or (dtype != xtype and xtype != torch.float32) or (
+            out_dtype is not None and out_dtype != dtype):
+        raise ValueError(f"x of {xtype}, y of {None if y is None else y.dtype}, out_dtype {out_dtype}: h has y's "
+                         "type, and that is x's or, next to an fp32 x, 16-bit")
+    if norm not in _NORMS or post_norm not in _NORMS:
+        raise ValueError(f"norm {norm!r}, post_norm {post_norm!r}: each one of {sorted(map(str, _NORMS))}")
+    if norm is None and (quantize or y is None):
+        raise ValueError("norm=None needs a y, and gives nothing to quantize")
+    _rows(x, "x", shape, dev, xtype)
+    ptype = None
+    if weight is not None or bias is not None or post_weight is not None:
+        ptype = _params((("weight", weight), ("bias", bias), ("post_weight", post_weight)), (C,), dtype, dev)
+    G, ptype = _tables((("gate", gate), ("scale", scale), ("shift", shift)), C, index, (B, N), dtype, dev, ptype)
+    _values(valid_len, "valid_len", (B,), dev, torch.int32)
+    strides = [x.stride(0), x.stride(1), 0, 0, 0, 0, 0, 0]
+    if y is not None:
+        _rows(y, "y", shape, dev, dtype)
+        if x_out is None:
+            x_out = x.new_empty(shape)
+        else:
+            _rows(x_out, "x_out", shape, dev, xtype, written=True)
+        strides[2:6] = y.stride(0), y.stride(1), x_out.stride(0), x_out.stride(1)
+    elif x_out is not None:
+        raise ValueError("x_out without a y: the residual stream does not change")
+    if norm is not None:
+        if quantize:
+            shape, kind = (B, N, -(-C // 16) * 16), torch.int8
+            if out_scale is None:
+                out_scale = x.new_empty((B, N), dtype=torch.float32)
+            else:
+                _values(out_scale, "out_scale", (B, N), dev, torch.float32)
+        else:
+            kind = dtype
+        if out is None:
+            out = x.new_empty(shape, dtype=kind)
+        else:
             _rows(out, "out", shape, dev, kind, written=True)
-            strides[6:8] = out.stride(0), out.stride(1)
-            if quantize and out_scale is None:
-                out_scale = torch.empty((B, N), dtype=torch.float32, device=dev)
-            if quantize:
-                _values(out_scale, "out_scale", (B, N), dev, (torch.float32,))
-        elif out is not None:
-            raise ValueError("out without a norm")
-        if out_scale is not None and not quantize:
-            raise ValueError("out_scale without quantize")
-        if B and N:
-            _check(lib().sba_residual_norm(
-                _ptr(x), _ptr(y), _ptr(x_out), _ptr(out), _ptr(out_scale), _DTYPES[x.dtype], _DTYPES[dtype], B, N, C,
-                (ctypes.c_int64 * 8)(*strides), _ptr(valid_len), _NORMS[norm], _ptr(weight), _ptr(bias),
-                _NORMS[post_norm], _ptr(post_weight), _ptr(gate), _ptr(scale), _ptr(shift), ptype, G, _ptr(index),
-                float(eps), _stream(stream)), "sba_residual_norm")
-        r = x if y is None else x_out
-        return (r, out, out_scale) if quantize else (r, out)
+        strides[6:8] = out.stride(0), out.stride(1)
+    elif out is not None:
+        raise ValueError("out without a norm")
+    if out_scale is not None and not quantize:
+        raise ValueError("out_scale without quantize")
+    if B and N:
+        _check(lib().sba_residual_norm(
+            x.data_ptr(), _raw(y), _raw(x_out), _raw(out), _raw(out_scale), _DTYPES[xtype], _DTYPES[dtype], B, N, C,
+            _Strides8(*strides), _raw(valid_len), _NORMS[norm], _raw(weight), _raw(bias), _NORMS[post_norm],
+            _raw(post_weight), _raw(gate), _raw(scale), _raw(shift), 2 if ptype is None else _DTYPES[ptype], G,
+            _raw(index), eps, torch._C._cuda_getCurrentRawStream(dev)), "sba_residual_norm")
+    r = x if y is None else x_out
+    return (r, out, out_scale) if quantize else (r, out)
 
 
-def token_quantize(x, codes=None, scales=None, stream=None):
+@_on_device
+def token_quantize(x, codes=None, scales=None):
     """Rows in 8 bits with one scale a row: scales = max|row| / 127, codes the nearest integers
     (see include/sba.h).  x: [..., K] of bf16, fp16 or fp32, [M, K] (tokens, or a weight's
     output channels), [B, N, K], or the attention's head layout [B, H, N, D], whose K = H * D;
     at any strides with contiguous rows.  Returns (codes int8 [M, K'] or [B, N, K'], scales
     fp32 [M] or [B, N]), K' = K rounded up to a multiple of 16 (zero codes)."""
-    with _place(x, stream):
-        if x.dim() not in (2, 3, 4) or x.dtype not in _DTYPES or (x.stride(-1) != 1 and x.shape[-1] > 1):
-            raise ValueError("x: expected [M, K], [B, N, K] or [B, H, N, D] in bf16, fp16 or fp32, its last dimension "
-                             "contiguous")
-        if x.dim() == 4:
-            (B, H, N, D), (sb, sh, sn) = x.shape, x.stride()[:3]
-        elif x.dim() == 3:
-            (B, N, D), (sb, sn), H, sh = x.shape, x.stride()[:2], 1, 0
-        else:
-            (N, D), sn, B, H, sb, sh = x.shape, x.stride(0), 1, 1, 0, 0
-        lead = (N,) if x.dim() == 2 else (B, N)
-        width = -(-(H * D) // 16) * 16
-        if codes is None:
-            codes = torch.empty((*lead, width), dtype=torch.int8, device=x.device)
-        if scales is None:
-            scales = torch.empty(lead, dtype=torch.float32, device=x.device)
-        _values(codes, "codes", (*lead, width), x.device, (torch.int8,))
-        _values(scales, "scales", lead, x.device, (torch.float32,))
-        if B and N:
-            _check(lib().sba_token_quantize(_ptr(x), _DTYPES[x.dtype], B, H, N, D, (ctypes.c_int64 * 3)(sb, sh, sn),
-                                            _ptr(codes), _ptr(scales), _stream(stream)), "sba_token_quantize")
-        return codes, scales
+    shape, strides = x.shape, x.stride()
+    kind = _DTYPES.get(x.dtype)
+    if kind is None or not 2 <= len(shape) <= 4 or (strides[-1] != 1 and shape[-1] > 1):
+        raise ValueError("x: expected [M, K], [B, N, K] or [B, H, N, D] in bf16, fp16 or fp32, its last dimension "
+                         "contiguous")
+    if len(shape) == 4:
+        (B, H, N, D), (sb, sh, sn, _) = shape, strides
+        lead = (B, N)
+    elif len(shape) == 3:
+        (B, N, D), (sb, sn, _), H, sh = shape, strides, 1, 0
+        lead = (B, N)
+    else:
+        (N, D), (sn, _), B, H, sb, sh = shape, strides, 1, 1, 0, 0
+        lead = (N,)
+    width = -(-(H * D) // 16) * 16
+    if codes is None:
+        codes = x.new_empty((*lead, width), dtype=torch.int8)
+    else:
+        _values(codes, "codes", (*lead, width), x.get_device(), torch.int8)
+    if scales is None:
+        scales = x.new_empty(lead, dtype=torch.float32)
+    else:
+        _values(scales, "scales", lead, x.get_device(), torch.float32)
+    if B and N:
+        _check(lib().sba_token_quantize(x.data_ptr(), kind, B, H, N, D, _Strides3(sb, sh, sn), codes.data_ptr(),
+                                        scales.data_ptr(), torch._C._cuda_getCurrentRawStream(x.get_device())), "sba_token_quantize")
+    return codes, scales
 
 
+@_on_device
 def int8_linear(codes, scales, weight_codes, weight_scales, bias=None, activation=None, gate=None, index=None,
-                residual=None, out_dtype=torch.bfloat16, heads=None, out=None, stream=None):
+                residual=None, out_dtype=torch.bfloat16, heads=None, out=None):
     """A projection in 8-bit integers with its epilogue (see include/sba.h):
 
       out = residual + gate * activation((codes @ weight_codes.T) * scales * weight_scales + bias)
@@ -667,44 +694,52 @@ def int8_linear(codes, scales, weight_codes, weight_scales, bias=None, activatio
     gate: [G, M], row b for sample b or row index[b, n]; both fp32 or of out's type.
     residual: of out's shape and type, contiguous rows, may be out.  Returns out [..., M]; with
     heads=H (and codes [B, N, K]) the attention's layout [B, H, N, M / H] instead."""
-    with _place(codes, stream):
-        dev = codes.device
-        if codes.dim() not in (2, 3) or codes.dtype != torch.int8 or not codes.is_contiguous():
-            raise ValueError("codes: expected a contiguous int8 tensor [N, K] or [B, N, K]")
-        lead, K = tuple(codes.shape[:-1]), codes.shape[-1]
-        B, N = lead if codes.dim() == 3 else (1, *lead)
-        if weight_codes.dim() != 2:
-            raise ValueError("weight_codes: expected [M, K]")
-        M = weight_codes.shape[0]
-        _values(scales, "scales", lead, dev, (torch.float32,))
-        _values(weight_codes, "weight_codes", (M, K), dev, (torch.int8,))
-        _values(weight_scales, "weight_scales", (M,), dev, (torch.float32,))
-        if out_dtype not in _DTYPES:
-            raise ValueError(f"out_dtype {out_dtype}: expected bf16, fp16 or fp32")
-        if activation not in _ACTS:
-            raise ValueError(f"unknown activation {activation!r}; one of {sorted(map(str, _ACTS))}")
-        if heads is not None and (codes.dim() != 3 or heads < 1 or M % heads or residual is not None):
-            raise ValueError("heads: codes [B, N, K], a divisor of M, and no residual")
-        G = _index_rows(index, (gate,), lead, B, dev)
-        ptype = _param_dtype((("bias", bias), ("gate", gate)), out_dtype, dev, {"bias": (M,), "gate": (G, M)})
-        shape = (B, heads, N, M // heads) if heads else (*lead, M)
-        if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=dev)
+    shape, dev = codes.shape, codes.get_device()
+    if len(shape) == 3:
+        B, N, K = shape
+        lead = (B, N)
+    elif len(shape) == 2:
+        (N, K), B = shape, 1
+        lead = (N,)
+    else:
+        raise ValueError("codes: expected [N, K] or [B, N, K]")
+    if weight_codes.dim() != 2:
+        raise ValueError("weight_codes: expected [M, K]")
+    M = weight_codes.shape[0]
+    _values(codes, "codes", shape, dev, torch.int8)
+    _values(scales, "scales", lead, dev, torch.float32)
+    _values(weight_codes, "weight_codes", (M, K), dev, torch.int8)
+    _values(weight_scales, "weight_scales", (M,), dev, torch.float32)
+    otype = _DTYPES.get(out_dtype)
+    if otype is None:
+        raise ValueError(f"out_dtype {out_dtype}: expected bf16, fp16 or fp32")
+    if activation not in _ACTS:
+        raise ValueError(f"unknown activation {activation!r}; one of {sorted(map(str, _ACTS))}")
+    if heads is not None and (len(lead) != 2 or heads < 1 or M % heads or residual is not None):
+        raise ValueError("heads: codes [B, N, K], a divisor of M, and no residual")
+    ptype, G = None, 0
+    if bias is not None:
+        ptype = _params((("bias", bias),), (M,), out_dtype, dev)
+    if gate is not None or index is not None:
+        G, ptype = _tables((("gate", gate),), M, index, lead, out_dtype, dev, ptype)
+    shape = (B, heads, N, M // heads) if heads else (*lead, M)
+    if out is None:
+        out = codes.new_empty(shape, dtype=out_dtype)
+    else:
         _rows(out, "out", shape, dev, out_dtype, written=True)
-        strides = [0] * 5
-        if residual is not None:
-            _rows(residual, "residual", shape, dev, out_dtype)
-            strides[:2] = residual.stride()[:2] if len(lead) == 2 else (0, residual.stride(0))
-        if heads:
-            strides[2:] = out.stride()[:3]
-        else:
-            strides[2:] = (out.stride(0), 0, out.stride(1)) if len(lead) == 2 else (0, 0, out.stride(0))
-        if B and N:
-            _check(lib().sba_int8_linear(
-                _ptr(codes), _ptr(scales), _ptr(weight_codes), _ptr(weight_scales), B, N, K, M, _ptr(bias), _ptr(gate),
-                ptype, G, _ptr(index), _ACTS[activation], _ptr(residual), _ptr(out), _DTYPES[out_dtype], heads or 0,
-                (ctypes.c_int64 * 5)(*strides), _stream(stream)), "sba_int8_linear")
-        return out
+    rb = rn = 0
+    if residual is not None:
+        _rows(residual, "residual", shape, dev, out_dtype)
+        rb, rn = residual.stride()[:2] if len(lead) == 2 else (0, residual.stride(0))
+    strides = out.stride()
+    ob, oh, on = strides[:3] if heads else (strides[0], 0, strides[1]) if len(lead) == 2 else (0, 0, strides[0])
+    if B and N:
+        _check(lib().sba_int8_linear(
+            codes.data_ptr(), scales.data_ptr(), weight_codes.data_ptr(), weight_scales.data_ptr(), B, N, K, M,
+            _raw(bias), _raw(gate), 2 if ptype is None else _DTYPES[ptype], G, _raw(index), _ACTS[activation],
+            _raw(residual), out.data_ptr(), otype, heads or 0, _Strides5(rb, rn, ob, oh, on),
+            torch._C._cuda_getCurrentRawStream(dev)), "sba_int8_linear")
+    return out
 
 
 class RopeTable:
@@ -724,6 +759,7 @@ class RopeTable:
         self.axes = max(self.axis) + 1
         self._freq = (ctypes.c_double * n)(*self.inv_freq)
         self._axis = (ctypes.c_uint8 * n)(*self.axis)
+        self._freq_at, self._axis_at = ctypes.addressof(self._freq), ctypes.addressof(self._axis)
 
 
 def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scaling=None, factor: float = 1.0,
@@ -764,35 +800,37 @@ def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scalin
     return RopeTable(freq * axes, [a for a in range(axes) for _ in range(d // 2)], amplitude)
 
 
-def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool = False, out=None, stream=None):
+@_on_device
+def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool = False, out=None):
     """Rotary positions (see include/sba.h): the first table.rope_dim channels of x [B, H, N, D]
     turned by the token's position, the others copied.  x: bf16, fp16 or fp32 at any strides
     with contiguous channels (a token-major [B, N, H, D] tensor is x.transpose(1, 2)).  pos:
     int32 [B, N, table.axes], or [B, N] for one axis.  layout: pairs of channels (2p, 2p + 1),
     "interleaved", or (p, p + rope_dim / 2), "half".  inverse turns back, which is also the
     gradient.  out may be x.  Returns out (laid out as x)."""
-    with _place(x, stream):
-        if x.dim() != 4 or x.dtype not in _DTYPES:
-            raise ValueError("x: expected [B, H, N, D] in bf16, fp16 or fp32")
-        B, H, N, D = x.shape
-        if layout not in _LAYOUTS:
-            raise ValueError(f"unknown layout {layout!r}; one of {sorted(_LAYOUTS)}")
-        if table.rope_dim > D:
-            raise ValueError(f"a table of {table.rope_dim} channels for heads of {D}")
-        _rows(x, "x", x.shape, x.device, x.dtype)
-        shape = (B, N) if pos.dim() == 2 and table.axes == 1 else (B, N, table.axes)
-        _values(pos, "pos", shape, x.device, (torch.int32,))
-        if out is None:
-            out = torch.empty_like(x)
-        _rows(out, "out", x.shape, x.device, x.dtype, written=True)
-        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+    shape, dev, strides = x.shape, x.get_device(), x.stride()
+    dtype = _DTYPES.get(x.dtype)
+    if len(shape) != 4 or dtype is None:
+        raise ValueError("x: expected [B, H, N, D] in bf16, fp16 or fp32")
+    B, H, N, D = shape
+    if layout not in _LAYOUTS:
+        raise ValueError(f"unknown layout {layout!r}; one of {sorted(_LAYOUTS)}")
+    if table.rope_dim > D:
+        raise ValueError(f"a table of {table.rope_dim} channels for heads of {D}")
+    _rows(x, "x", shape, dev, x.dtype)
+    _values(pos, "pos", (B, N) if pos.dim() == 2 and table.axes == 1 else (B, N, table.axes), dev, torch.int32)
+    if out is None:
+        out = torch.empty_like(x)  # of an expanded x: dense
+    else:
+        _rows(out, "out", shape, dev, x.dtype, written=True)
+        if out.data_ptr() == x.data_ptr() and out.stride() != strides:
             raise ValueError("out at x's place with other strides")
-        if B and H and N:
-            _check(lib().sba_rotary(_ptr(x), _ptr(out), _DTYPES[x.dtype], _ptr(pos), table.axes, B, H, N, D,
-                                    (ctypes.c_int64 * 6)(*x.stride()[:3], *out.stride()[:3]), table.rope_dim,
-                                    _LAYOUTS[layout], ctypes.addressof(table._freq), ctypes.addressof(table._axis),
-                                    table.amplitude, int(inverse), _stream(stream)), "sba_rotary")
-        return out
+    if B and H and N:
+        _check(lib().sba_rotary(x.data_ptr(), out.data_ptr(), dtype, pos.data_ptr(), table.axes, B, H, N, D,
+                                _Strides6(*strides[:3], *out.stride()[:3]), table.rope_dim, _LAYOUTS[layout],
+                                table._freq_at, table._axis_at, table.amplitude, int(inverse),
+                                torch._C._cuda_getCurrentRawStream(dev)), "sba_rotary")
+    return out
 
 
 def device_status(stream=None) -> int:
