@@ -234,7 +234,7 @@ __device__ __forceinline__ void param_load(uint64_t (&f)[4], const char* base, i
 // Sum or maximum over the threads of a row: a warp's, or a CTA's.  `slot` alternates between
 // calls, so one barrier per reduction suffices.
 template <bool WARP, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float (*red)[16], int& slot) {
+__device__ __forceinline__ float row_reduce(float v, float (*red)[32], int& slot) {
     if (MAX) {  // of values that are not negative: their bits are in their order
         v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
     } else {
@@ -246,14 +246,11 @@ __device__ __forceinline__ float row_reduce(float v, float (*red)[16], int& slot
         if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = v;
         __syncthreads();
         const float4* r = reinterpret_cast<const float4*>(red[slot]);
-        const float4 a = r[0], b = r[1];
-        v = MAX ? fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)))
-                : ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
-        if (blockDim.x > 256) {
-            const float4 c = r[2], d = r[3];
-            const float w = MAX ? fmaxf(fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)), fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)))
-                                : ((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w));
-            v = MAX ? fmaxf(v, w) : v + w;
+        for (int i = 0; i < (int)blockDim.x; i += 256) {  // eight warps
+            const float4 a = r[i / 128], b = r[i / 128 + 1];
+            const float w = MAX ? fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)))
+                                : ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+            v = i == 0 ? w : MAX ? fmaxf(v, w) : v + w;
         }
         slot ^= 1;
     }
@@ -264,7 +261,7 @@ __device__ __forceinline__ float row_reduce(float v, float (*red)[16], int& slot
 // subtracted).  Columns past C hold 0 on entry and on return.
 template <bool WARP, int VPT, bool VEC>
 __device__ __forceinline__ float row_statistics(uint64_t (&f)[VPT][4], bool centre, const RowPlace& q, float inv_c,
-                                                float eps, float (*red)[16], int& slot) {
+                                                float eps, float (*red)[32], int& slot) {
     float a, b;
     if (centre) {
         uint64_t s = pack2(0.f, 0.f);
@@ -341,16 +338,20 @@ enum RowKind : int {
 // XT, HT: the types of x and r, and of y and h (as RowType).  WARP: four rows per CTA of four
 // warps; otherwise a row per CTA, and as many CTAs as are resident.  P32: parameters in fp32.
 template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32>
-__global__ void __launch_bounds__(WARP ? 128 : VPT > 4 ? 512 : 256, WARP ? 4 : VPT > 4 ? 1 : 2) residual_norm_kernel(
+__global__ void __launch_bounds__(WARP                  ? 128
+                                  : KIND == kRowQuant || KIND == kRowQuantHeads ? 1024
+                                  : VPT > 4                                     ? 512
+                                                                                : 256,
+                                  WARP ? 4 : VPT > 4 || KIND == kRowQuant || KIND == kRowQuantHeads ? 1 : 2) residual_norm_kernel(
     const __grid_constant__ RowParams p) {
-    __shared__ __align__(16) float red[2][16];
+    __shared__ __align__(16) float red[2][32];
     int slot = 0;
     const int tpr = WARP ? 32 : blockDim.x;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     constexpr int rpc = WARP ? 4 : 1;
     const uint32_t rows = (uint32_t)p.rows, N = (uint32_t)p.N, stride = gridDim.x * rpc;
     if (!WARP) {
-        if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+        for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i >> 5][i & 31] = 0.f;
         __syncthreads();
     }
     constexpr bool kAny = KIND == kRowAny;

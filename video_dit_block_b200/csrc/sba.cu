@@ -807,13 +807,17 @@ template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32 = tru
 sba_status launch_rows(const sba::RowParams& p, int chunks, cudaStream_t s) {
     const auto kernel = sba::residual_norm_kernel<XT, HT, WARP, VPT, VEC, KIND, P32>;
     const int threads = WARP ? 128 : (chunks + 32 * VPT - 1) / (32 * VPT) * 32;
-    int dev = 0, sms = 0, resident = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, 0) != cudaSuccess)
-        return SBA_ERR_CUDA;
-    const long long ctas = WARP ? (p.rows + 3) / 4 : p.rows, most = (long long)sms * resident;
-    kernel<<<(unsigned)(ctas < most ? ctas : most), threads, 0, s>>>(p);
+    const long long ctas = WARP ? (p.rows + 3) / 4 : p.rows;
+    long long grid = ctas;
+    if (ctas > 128) {
+        int dev = 0, sms = 0, resident = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, 0) != cudaSuccess || resident < 1)
+            return SBA_ERR_CUDA;
+        if (ctas > (long long)sms * resident) grid = (long long)sms * resident;
+    }
+    kernel<<<(unsigned)grid, threads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
 }
 
@@ -849,12 +853,12 @@ sba_status run_rows(const sba::RowParams& p, bool vec, cudaStream_t s) {
     }
     if (chunks <= 32) return launch_rows<XT, HT, true, 1, true, sba::kRowAny>(p, chunks, s);
     if (chunks <= 128) return launch_rows<XT, HT, true, 4, true, sba::kRowAny>(p, chunks, s);
-    if (chunks > 1024) return launch_rows<XT, HT, false, 8, true, sba::kRowAny>(p, chunks, s);
     if constexpr (XT == HT) {
         if (row_kind(p) == sba::kRowQuant) return launch_rows<XT, HT, false, 4, true, sba::kRowQuant>(p, chunks, s);
         if (row_kind(p) == sba::kRowQuantHeads)
             return launch_rows<XT, HT, false, 4, true, sba::kRowQuantHeads>(p, chunks, s);
     }
+    if (chunks > 1024) return launch_rows<XT, HT, false, 8, true, sba::kRowAny>(p, chunks, s);
     if constexpr (HT != sba::kRowFp32) return p.param32 ? run_kind<XT, HT, true>(p, chunks, s) : run_kind<XT, HT, false>(p, chunks, s);
     return launch_rows<XT, HT, false, 4, true, sba::kRowAny>(p, chunks, s);
 }
