@@ -1127,7 +1127,7 @@ extern "C" sba_status sba_rotary(const void* x, void* out, int dtype, const int3
         const long double scaled = std::floor(t * 18446744073709551616.0L + 0.5L);
         p.turn[i] = scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
     }
-    const bool vec = D % 16 == 0 && p.pairs % 8 == 0 && rows16(x, strides, 3, w) && rows16(out, strides + 3, 3, w);
+    const bool vec = D % 16 == 0 && p.pairs % (p.half ? 8 : 4) == 0 && rows16(x, strides, 3, w) && rows16(out, strides + 3, 3, w);
     const long long per_token = vec ? D / 16 : (p.copy ? D - p.pairs : p.pairs);
     const long long gx = ((long long)N * per_token + 255) / 256;
     if (gx > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
@@ -1142,8 +1142,10 @@ extern "C" sba_status sba_rotary(const void* x, void* out, int dtype, const int3
     const dim3 grid((unsigned)gx, (unsigned)((H + hpc - 1) / hpc), (unsigned)B);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (vec) {
-        if (dtype == SBA_DTYPE_FP32) sba::rotary_vec_kernel<true><<<grid, 256, 0, s>>>(p);
-        else sba::rotary_vec_kernel<false><<<grid, 256, 0, s>>>(p);
+        if (dtype == SBA_DTYPE_FP32 && p.half) sba::rotary_vec_kernel<true, true><<<grid, 256, 0, s>>>(p);
+        else if (dtype == SBA_DTYPE_FP32) sba::rotary_vec_kernel<true, false><<<grid, 256, 0, s>>>(p);
+        else if (p.half) sba::rotary_vec_kernel<false, true><<<grid, 256, 0, s>>>(p);
+        else sba::rotary_vec_kernel<false, false><<<grid, 256, 0, s>>>(p);
     } else {
         if (dtype == SBA_DTYPE_FP32) sba::rotary_any_kernel<true><<<grid, 256, 0, s>>>(p);
         else sba::rotary_any_kernel<false><<<grid, 256, 0, s>>>(p);
