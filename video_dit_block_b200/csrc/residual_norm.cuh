@@ -97,71 +97,79 @@ __device__ __forceinline__ void stg_stream(void* p, const uint4& v) {
 // How a kernel holds its rows.  T: 0 bf16, 1 fp16, 2 fp32.
 enum RowType : int { kRowBf16 = 0, kRowFp16 = 1, kRowFp32 = 2 };
 
-// Where element e of chunk v of thread t stands: with VEC eight neighbours per thread,
-// otherwise (rows whose address or length rules 16-byte accesses out) one neighbour per
-// thread, so that a warp's single-element accesses coalesce.  tpr: threads of a row.
+// A thread's place in its row: chunk v of thread t holds the 8 channels from row_col on.  With
+// VEC rows start on 16 bytes and C is a multiple of 8, so a chunk lies in the row (the first
+// `live` ones) or past it.  Otherwise the chunks start `a` channels before the row, at the 16
+// bytes that its first channel lies in, so that all but the row's two ends move in 16-byte
+// accesses just the same; `a` differs from row to row.
+struct RowPlace {
+    int t, tpr, C, live, a;
+};
 template <bool VEC>
-__device__ __forceinline__ int row_col(int v, int t, int tpr, int e) {
-    return VEC ? (v * tpr + t) * 8 + e : (v * 8 + e) * tpr + t;
+__device__ __forceinline__ int row_col(int v, const RowPlace& q) {
+    return (v * q.tpr + q.t) * 8 - (VEC ? 0 : q.a);
 }
+template <bool VEC>
+__device__ __forceinline__ bool row_full(int v, const RowPlace& q) {
+    const int c = row_col<VEC>(v, q);
+    return VEC ? v < q.live : c >= 0 && c + 8 <= q.C;
+}
+__device__ __forceinline__ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Eight values of a row as loaded: one 16-byte word of 16-bit values, two of fp32; without
-// VEC a 32-bit word each.
-template <int T, bool VEC>
+// Eight values of a row as loaded: one 16-byte word of 16-bit values, two of fp32.
+template <int T>
 struct Raw8 {
-    static constexpr int kWords = T == kRowFp32 || !VEC ? 2 : 1;
+    static constexpr int kWords = T == kRowFp32 ? 2 : 1;
     uint4 w[kWords];
 };
 
-// A thread's place in its row.  `live`: with VEC, its chunks that lie in the row (the first
-// ones: C is a multiple of 8 there).
-struct RowPlace {
-    int t, tpr, C, live;
-};
-template <bool VEC>
-__device__ __forceinline__ bool row_has(const RowPlace& q, int v, int e) {
-    return VEC ? v < q.live : row_col<false>(v, q.t, q.tpr, e) < q.C;
+// Values outside the row are zeros.  W: bytes a value.
+template <int T>
+__device__ __forceinline__ Raw8<T> row_edge(const char* base, int c, int C) {
+    uint32_t u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool in = (unsigned)(c + e) < (unsigned)C;
+        uint32_t x = 0;
+        if (in) x = T == kRowFp32 ? reinterpret_cast<const uint32_t*>(base)[c + e] : reinterpret_cast<const uint16_t*>(base)[c + e];
+        if (T == kRowFp32) u[e] = x;
+        else if (e & 1) u[e / 2] |= x << 16;
+        else u[e / 2] = x;
+    }
+    Raw8<T> r;
+    r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    if (T == kRowFp32) r.w[Raw8<T>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
+    return r;
 }
-
-// Columns past C give zeros.
 template <int T, bool VEC>
-__device__ __forceinline__ void row_load(Raw8<T, VEC>& raw, const char* base, int v, const RowPlace& q) {
+__device__ __forceinline__ void row_load(Raw8<T>& raw, const char* base, int v, const RowPlace& q) {
     constexpr int W = T == kRowFp32 ? 4 : 2;
-    if (VEC) {
-        const char* p = base + (v * q.tpr + q.t) * (8 * W);
+    const int c = row_col<VEC>(v, q);
+    const char* p = base + c * W;
+    if (row_full<VEC>(v, q) && (VEC || on16(p))) {
 #pragma unroll
-        for (int i = 0; i < Raw8<T, VEC>::kWords; ++i)
-            raw.w[i] = v < q.live ? ldg_stream(p + 16 * i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < Raw8<T>::kWords; ++i) raw.w[i] = ldg_stream(p + 16 * i);
+    } else if (!VEC && c < q.C) {
+        raw = row_edge<T>(base, c, q.C);
     } else {
-        uint32_t u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = row_col<false>(v, q.t, q.tpr, e);
-            u[e] = 0;
-            if (c < q.C)
-                u[e] = W == 4 ? reinterpret_cast<const uint32_t*>(base)[c] : reinterpret_cast<const uint16_t*>(base)[c];
-        }
-        raw.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        raw.w[Raw8<T, VEC>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
+        for (int i = 0; i < Raw8<T>::kWords; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
 // As four packed pairs of floats.
-template <int T, bool VEC>
-__device__ __forceinline__ void row_values(const Raw8<T, VEC>& raw, uint64_t (&f)[4]) {
-    const uint4 a = raw.w[0], b = raw.w[Raw8<T, VEC>::kWords - 1];
+template <int T>
+__device__ __forceinline__ void row_values(const Raw8<T>& raw, uint64_t (&f)[4]) {
+    const uint4 a = raw.w[0], b = raw.w[Raw8<T>::kWords - 1];
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float lo, hi, none;
+        float lo, hi;
         if (T == kRowFp32) {
             lo = __uint_as_float(u[2 * i]);
             hi = __uint_as_float(u[2 * i + 1]);
-        } else if (VEC) {
-            unpack16(u[i], T, lo, hi);
         } else {
-            unpack16(u[2 * i], T, lo, none);
-            unpack16(u[2 * i + 1], T, hi, none);
+            unpack16(u[i], T, lo, hi);
         }
         f[i] = pack2(lo, hi);
     }
@@ -173,58 +181,82 @@ __device__ __forceinline__ void row_store(char* base, const uint64_t (&f)[4], in
     float g[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack2(f[i], g[2 * i], g[2 * i + 1]);
-    if (VEC) {
-        if (v >= q.live) return;
-        char* p = base + (v * q.tpr + q.t) * (8 * W);
-        if (T == kRowFp32) {
-            stg_stream(p, make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
-                                     __float_as_uint(g[3])));
-            stg_stream(p + 16, make_uint4(__float_as_uint(g[4]), __float_as_uint(g[5]), __float_as_uint(g[6]),
-                                          __float_as_uint(g[7])));
-        } else {
-            stg_stream(p, make_uint4(pack16(g[0], g[1], T), pack16(g[2], g[3], T), pack16(g[4], g[5], T),
-                                     pack16(g[6], g[7], T)));
-        }
-    } else {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = T == kRowFp32 ? __float_as_uint(g[i]) : i < 4 ? pack16(g[2 * i], g[2 * i + 1], T) : 0u;
+    const int c = row_col<VEC>(v, q);
+    char* p = base + c * W;
+    if (row_full<VEC>(v, q) && (VEC || on16(p))) {
+        stg_stream(p, make_uint4(u[0], u[1], u[2], u[3]));
+        if (T == kRowFp32) stg_stream(p + 16, make_uint4(u[4], u[5], u[6], u[7]));
+    } else if (!VEC && c < q.C) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = row_col<false>(v, q.t, q.tpr, e);
-            if (c >= q.C) continue;
-            if (T == kRowFp32) reinterpret_cast<float*>(base)[c] = g[e];
-            else reinterpret_cast<uint16_t*>(base)[c] = (uint16_t)pack16(g[e], 0.f, T);
+            if ((unsigned)(c + e) >= (unsigned)q.C) continue;
+            if (T == kRowFp32) reinterpret_cast<uint32_t*>(base)[c + e] = u[e];
+            else reinterpret_cast<uint16_t*>(base)[c + e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
         }
     }
 }
 
-// Eight parameters of the same columns, through L1: fp32, or 16-bit of type T16.  Columns past
-// C give 0.
+// Eight parameters of the same columns, through L1: fp32, or 16-bit of type T16.  Columns
+// outside the row give 0.
 template <int T16, bool VEC>
 __device__ __forceinline__ void param_load(uint64_t (&f)[4], const char* base, int param32, int v, const RowPlace& q) {
     float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int c = row_col<VEC>(v, q);
     if (VEC) {
         if (v < q.live) {
             if (param32) {
                 // 32 bytes at once: two loads of 16 at a stride of 32 would each touch every line
                 asm("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                     : "=f"(g[0]), "=f"(g[1]), "=f"(g[2]), "=f"(g[3]), "=f"(g[4]), "=f"(g[5]), "=f"(g[6]), "=f"(g[7])
-                    : "l"(base + (v * q.tpr + q.t) * 32));
+                    : "l"(base + c * 4));
             } else {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(base + (v * q.tpr + q.t) * 16));
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(base + c * 2));
                 unpack16(w.x, T16, g[0], g[1]);
                 unpack16(w.y, T16, g[2], g[3]);
                 unpack16(w.z, T16, g[4], g[5]);
                 unpack16(w.w, T16, g[6], g[7]);
             }
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = row_col<false>(v, q.t, q.tpr, e);
-            float none;
-            if (c < q.C) {
-                if (param32) g[e] = __ldg(reinterpret_cast<const float*>(base) + c);
-                else unpack16(__ldg(reinterpret_cast<const uint16_t*>(base) + c), T16, g[e], none);
+    } else if (c < q.C) {
+        // the 16-byte words that the eight lie in, where those are all the row's, shifted; the
+        // shift is the same for all threads
+        const int PW = param32 ? 4 : 2, s = (int)((reinterpret_cast<uintptr_t>(base) + c * PW) & 15) / PW;
+        const bool inside = c - s >= 0 && c - s + (param32 ? 12 : 16) <= q.C;
+        const char* p = base + (c - s) * PW;
+        if (!inside) {
+            if (param32) {
+                const Raw8<kRowFp32> r = row_edge<kRowFp32>(base, c, q.C);
+                row_values<kRowFp32>(r, f);
+            } else {
+                const Raw8<T16 == kRowFp32 ? kRowBf16 : T16> r = row_edge<T16 == kRowFp32 ? kRowBf16 : T16>(base, c, q.C);
+                row_values<T16 == kRowFp32 ? kRowBf16 : T16>(r, f);
             }
+            return;
+        }
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p)), y = __ldg(reinterpret_cast<const uint4*>(p + 16));
+        uint32_t w[12] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, 0, 0, 0, 0};
+        if (param32) {
+            const uint4 z = __ldg(reinterpret_cast<const uint4*>(p + 32));
+            w[8] = z.x; w[9] = z.y; w[10] = z.z; w[11] = z.w;
+        }
+        const int ws = param32 ? s : s >> 1;
+        if (ws & 1) {
+#pragma unroll
+            for (int i = 0; i < 11; ++i) w[i] = w[i + 1];
+        }
+        if (ws & 2) {
+#pragma unroll
+            for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+        }
+        if (param32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack16(s & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i], T16, g[2 * i], g[2 * i + 1]);
         }
     }
 #pragma unroll
@@ -274,15 +306,16 @@ __device__ __forceinline__ float row_statistics(uint64_t (&f)[VPT][4], bool cent
         const float mean = row_reduce<WARP, false>(a + b, red, slot) * inv_c;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            if (VEC) {
-                const float m = v < q.live ? -mean : 0.f;
+            if (VEC || row_full<VEC>(v, q)) {
+                const float m = !VEC || v < q.live ? -mean : 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[v][i] = fadd2(f[v][i], pack2(m, m));
             } else {
+                const int c = row_col<VEC>(v, q);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    f[v][i] = fadd2(f[v][i], pack2(row_has<false>(q, v, 2 * i) ? -mean : 0.f,
-                                                   row_has<false>(q, v, 2 * i + 1) ? -mean : 0.f));
+                    f[v][i] = fadd2(f[v][i], pack2((unsigned)(c + 2 * i) < (unsigned)q.C ? -mean : 0.f,
+                                                   (unsigned)(c + 2 * i + 1) < (unsigned)q.C ? -mean : 0.f));
             }
         }
     }
@@ -345,8 +378,10 @@ __global__ void __launch_bounds__(WARP                  ? 128
                                   WARP ? 4 : VPT > 4 || KIND == kRowQuant || KIND == kRowQuantHeads ? 1 : 2) residual_norm_kernel(
     const __grid_constant__ RowParams p) {
     __shared__ __align__(16) float red[2][32];
+    extern __shared__ __align__(16) unsigned char code_rows[];  // without VEC: a row's codes
     int slot = 0;
     const int tpr = WARP ? 32 : blockDim.x;
+    unsigned char* codes = code_rows + (WARP ? (threadIdx.x >> 5) * (32 * VPT * 8) : 0);
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     constexpr int rpc = WARP ? 4 : 1;
     const uint32_t rows = (uint32_t)p.rows, N = (uint32_t)p.N, stride = gridDim.x * rpc;
@@ -367,22 +402,30 @@ __global__ void __launch_bounds__(WARP                  ? 128
     const bool quant = kAny ? p.quant != 0 : KIND == kRowQuant || KIND == kRowQuantHeads || KIND == kRowNormQuant || KIND == kRowGateNormQuant;
     const bool heads = kAny ? p.D != 0 : KIND == kRowQuantHeads;
     constexpr int XW = XT == kRowFp32 ? 4 : 2, HW = HT == kRowFp32 ? 4 : 2;
-    const RowPlace q{t, tpr, p.C, min(VPT, max(0, (p.C / 8 - t + tpr - 1) / tpr))};
+    RowPlace q{t, tpr, p.C, min(VPT, max(0, (p.C / 8 - t + tpr - 1) / tpr)), 0};
     const float inv_c = 1.f / (float)p.C;
-    Raw8<XT, VEC> rx[VPT];
-    Raw8<HT, VEC> ry[VPT];
+    Raw8<XT> rx[VPT];
+    Raw8<HT> ry[VPT];
 
     // A row's place in the tensors.  Rows step by the grid, within a sample by adding to the
     // addresses: finding each row anew took more instructions than a warp's channels did.
     struct At {
         uint32_t row, n;
-        int b, len;
+        int b, len, a;
         const char *x, *y;
         char *r, *h;
     };
     const int h_width = quant ? 1 : HW;
     const long long dx = stride * p.x_sn * XW, dy = stride * p.y_sn * HW, dr = stride * p.r_sn * XW,
                     dh = stride * p.h_sn * h_width;
+    // where the chunks start: by the narrowest tensor, the others mostly agree with it
+    auto place = [&](At& a) {
+        if (VEC || heads) a.a = 0;
+        else if (XT == HT) a.a = (int)(reinterpret_cast<uintptr_t>(a.x) & 15) / XW;
+        else if (has_y) a.a = (int)(reinterpret_cast<uintptr_t>(a.y) & 15) / HW;
+        else if (!quant) a.a = (int)(reinterpret_cast<uintptr_t>(a.h) & 15) / HW;
+        else a.a = (int)(reinterpret_cast<uintptr_t>(a.x) & 15) / XW;
+    };
     auto seek = [&](At& a) {
         a.b = (int)(a.row / N);
         a.n = a.row - a.b * N;
@@ -391,6 +434,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
         a.y = static_cast<const char*>(p.y) + (a.b * p.y_sb + a.n * p.y_sn) * HW;
         a.r = static_cast<char*>(p.r) + (a.b * p.r_sb + a.n * p.r_sn) * XW;
         a.h = static_cast<char*>(p.h) + (a.b * p.h_sb + a.n * p.h_sn) * h_width;
+        place(a);
     };
     auto step = [&](At& a) {
         a.row += stride;
@@ -400,6 +444,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
             a.y += dy;
             a.r += dr;
             a.h += dh;
+            place(a);
         } else if (a.row < rows) {
             seek(a);
         }
@@ -407,40 +452,37 @@ __global__ void __launch_bounds__(WARP                  ? 128
     // the loads of a row (padding is not read)
     auto load = [&](const At& a) {
         if (a.row >= rows || (int)a.n >= a.len) return;
-        if (!heads) {
+        RowPlace qa = q;
+        qa.a = a.a;
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_load<XT, VEC>(rx[v], a.x, v, q);
-        } else if (VEC) {
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int hd = row_col<true>(v, t, tpr, 0) / p.D;
+        for (int v = 0; v < VPT; ++v) {
+            if (!heads) {
+                row_load<XT, VEC>(rx[v], a.x, v, qa);
+            } else if (VEC) {
+                const int hd = row_col<true>(v, q) / p.D;
                 // the head's row, moved back so that column c of it is channel c % D
-                row_load<XT, VEC>(rx[v], a.x + hd * (p.x_sh - p.D) * XW, v, q);
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                uint32_t u[8];
+                row_load<XT, VEC>(rx[v], a.x + hd * (p.x_sh - p.D) * XW, v, qa);
+            } else {
+                const int c = row_col<true>(v, q);
+                uint32_t u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int c = row_col<false>(v, t, tpr, e);
-                    u[e] = 0;
-                    if (c < p.C) {
-                        const char* at = a.x + ((c / p.D) * p.x_sh + c % p.D) * XW;
-                        u[e] = XW == 4 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-                    }
+                    if (c + e >= p.C) continue;
+                    const char* at = a.x + ((c + e) / p.D * p.x_sh + (c + e) % p.D) * XW;
+                    if (XW == 4) u[e] = *reinterpret_cast<const uint32_t*>(at);
+                    else u[e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(at) << (16 * (e & 1));
                 }
                 rx[v].w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-                rx[v].w[Raw8<XT, VEC>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
+                if (XW == 4) rx[v].w[Raw8<XT>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
             }
         }
         if (has_y) {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_load<HT, VEC>(ry[v], a.y, v, q);
+            for (int v = 0; v < VPT; ++v) row_load<HT, VEC>(ry[v], a.y, v, qa);
         }
     };
 
-    constexpr bool kAhead = VEC && VPT <= 4;  // registers for a second row
+    constexpr bool kAhead = VPT <= 4;  // registers for a second row
     At next;
     next.row = blockIdx.x * rpc + (WARP ? threadIdx.x >> 5 : 0);
     if (next.row >= rows) return;
@@ -448,6 +490,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
     load(next);
     while (next.row < rows) {
         const At at = next;
+        q.a = at.a;
         step(next);
         uint64_t f[VPT][4];
         if ((int)at.n >= at.len) {
@@ -481,7 +524,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
         if (has_y) {
             uint64_t z[VPT][4];
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_values<HT, VEC>(ry[v], z[v]);
+            for (int v = 0; v < VPT; ++v) row_values<HT>(ry[v], z[v]);
             float inv = 1.f;
             if (has_post) inv = row_statistics<WARP, VPT, VEC>(z, p.post == kNormLayer, q, inv_c, p.eps, red, slot);
             if (has_post) {
@@ -494,7 +537,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
                 if (p.post_weight) row_step<kStepMul, HT, VPT, VEC>(z, z, static_cast<const char*>(p.post_weight), param32, q);
             }
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_values<XT, VEC>(rx[v], f[v]);
+            for (int v = 0; v < VPT; ++v) row_values<XT>(rx[v], f[v]);
             if (has_gate) {
                 row_step<kStepGate, HT, VPT, VEC>(f, z, static_cast<const char*>(p.gate) + goff, param32, q);
             } else {
@@ -508,7 +551,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
             for (int v = 0; v < VPT; ++v) row_store<XT, VEC>(at.r, f[v], v, q);
         } else {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_values<XT, VEC>(rx[v], f[v]);
+            for (int v = 0; v < VPT; ++v) row_values<XT>(rx[v], f[v]);
         }
 
         // the next row's loads run under this one's statistics and stores
@@ -594,21 +637,28 @@ __global__ void __launch_bounds__(WARP                  ? 128
                 code[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(lo, inv), kMagic));
                 code[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(hi, inv), kMagic));
             }
+            uint2 w;
+            w.x = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
+            w.y = __byte_perm(__byte_perm(code[4], code[5], 0x0040), __byte_perm(code[6], code[7], 0x0040), 0x5410);
+            const int k = (v * tpr + t) * 8;
             if (VEC) {
-                const int c = row_col<true>(v, t, tpr, 0);
-                if (c < p.Cq) {
-                    uint2 w;
-                    w.x = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
-                    w.y = __byte_perm(__byte_perm(code[4], code[5], 0x0040), __byte_perm(code[6], code[7], 0x0040), 0x5410);
-                    *reinterpret_cast<uint2*>(at.h + c) = w;
-                }
+                if (k < p.Cq) *reinterpret_cast<uint2*>(at.h + k) = w;
             } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int c = row_col<false>(v, t, tpr, e);
-                    if (c < p.Cq) at.h[c] = (char)code[e];
-                }
+                *reinterpret_cast<uint2*>(codes + k) = w;
             }
+        }
+        if (!VEC) {
+            // the codes stand `a` bytes late in shared memory: out in aligned words
+            if (WARP) __syncwarp();
+            else __syncthreads();
+            for (int c = 16 * t; c < p.Cq; c += 16 * tpr) {
+                const uint32_t* s = reinterpret_cast<const uint32_t*>(codes + c + (q.a & ~3));
+                const int sh = 8 * (q.a & 3);
+                *reinterpret_cast<uint4*>(at.h + c) =
+                    make_uint4(__funnelshift_r(s[0], s[1], sh), __funnelshift_r(s[1], s[2], sh),
+                               __funnelshift_r(s[2], s[3], sh), __funnelshift_r(s[3], s[4], sh));
+            }
+            if (WARP) __syncwarp();  // (a CTA's next row has a reduction before its codes)
         }
         if (!kAhead) load(next);
     }

@@ -809,15 +809,16 @@ sba_status launch_rows(const sba::RowParams& p, int chunks, cudaStream_t s) {
     const int threads = WARP ? 128 : (chunks + 32 * VPT - 1) / (32 * VPT) * 32;
     const long long ctas = WARP ? (p.rows + 3) / 4 : p.rows;
     long long grid = ctas;
+    const size_t smem = VEC || !p.quant ? 0 : (size_t)threads * VPT * 8;  // the codes of the CTA's rows
     if (ctas > 128) {
         int dev = 0, sms = 0, resident = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, 0) != cudaSuccess || resident < 1)
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem) != cudaSuccess || resident < 1)
             return SBA_ERR_CUDA;
         if (ctas > (long long)sms * resident) grid = (long long)sms * resident;
     }
-    kernel<<<(unsigned)grid, threads, 0, s>>>(p);
+    kernel<<<(unsigned)grid, threads, smem, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
 }
 
@@ -848,8 +849,15 @@ template <int XT, int HT>
 sba_status run_rows(const sba::RowParams& p, bool vec, cudaStream_t s) {
     const int chunks = p.quant ? p.Cq / 8 : (p.C + 7) / 8;
     if (!vec) {
-        if (chunks <= 128) return launch_rows<XT, HT, true, 4, false, sba::kRowAny>(p, chunks, s);
-        return launch_rows<XT, HT, false, 8, false, sba::kRowAny>(p, chunks, s);
+        // the row may start up to 7 channels into its first chunk, and its codes are read back
+        // up to 4 bytes past their end
+        const int most = chunks + 2;
+        if (most <= 128) return launch_rows<XT, HT, true, 4, false, sba::kRowAny>(p, most, s);
+        if constexpr (XT == HT)
+            if (row_kind(p) == sba::kRowQuant && most <= 4096)
+                return launch_rows<XT, HT, false, 4, false, sba::kRowQuant>(p, most, s);
+        if (most <= 1024) return launch_rows<XT, HT, false, 4, false, sba::kRowAny>(p, most, s);
+        return launch_rows<XT, HT, false, 9, false, sba::kRowAny>(p, most, s);
     }
     if (chunks <= 32) return launch_rows<XT, HT, true, 1, true, sba::kRowAny>(p, chunks, s);
     if (chunks <= 128) return launch_rows<XT, HT, true, 4, true, sba::kRowAny>(p, chunks, s);
