@@ -223,8 +223,9 @@ __device__ __forceinline__ float linear_act(float v, int act) {
 }
 
 // v of columns n .. n + U - 1 of a row, before the residual; `sw` and `bias` are those
-// columns' (bias 0 where there is none).
-template <int U>
+// columns' (bias 0 where there is none).  WIDE: all of them inside N, the gate's rows on 16
+// bytes.
+template <int U, bool WIDE>
 __device__ __forceinline__ void linear_value(float (&v)[U], const LinearParams& p, const LinearRow& r, int n,
                                              const uint32_t* acc, const float* sw, const float* bias) {
 #pragma unroll
@@ -244,10 +245,16 @@ __device__ __forceinline__ void linear_value(float (&v)[U], const LinearParams& 
         for (int i = 0; i < U; ++i) v[i] = linear_act(v[i], p.act);
     }
     if (r.gate) {
-        float t[U];
-        linear_load<U>(t, r.gate, n, p.param_type);
+        if (WIDE) {
+            float t[U];
+            linear_load<U>(t, r.gate, n, p.param_type);
 #pragma unroll
-        for (int i = 0; i < U; ++i) v[i] *= t[i];
+            for (int i = 0; i < U; ++i) v[i] *= t[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (n + i < p.N) v[i] *= linear_load1(r.gate, n + i, p.param_type);
+        }
     }
 }
 // The offset of column n in its output row.
@@ -305,11 +312,13 @@ __device__ __forceinline__ void pair_tile(int i, int tiles_m, int tiles_n, int& 
 // A lane of an epilogue warp has a row of the accumulator, but 32 lanes storing to 32 rows
 // take 32 cycles an access and held the tile back (11,600 cycles a tile; 25,000 with a
 // residual).  So the rows pass through 2 KB of shared memory in pieces of 64 bytes a row
-// (32 columns of 16 bits, 16 of fp32), and four lanes move one row's piece.  16-byte word j of row r
-// stands at 4 r + (j ^ (r / 2 & 3)): eight lanes touch all banks either way.
+// (32 columns of 16 bits, 16 of fp32), and neighbouring lanes move neighbouring columns: 16
+// bytes each, four lanes a row, or (rows off the 16-byte grid, or past the last column) one
+// column each.  16-byte word j of row r stands at 4 r + (j ^ (r / 2 & 3)): eight lanes touch all
+// banks either way.
 __device__ __forceinline__ int pair_word(int r, int j) { return 4 * r + (j ^ ((r >> 1) & 3)); }
 
-// The residual of the piece at column n, as this lane moves it.
+// The residual of the piece at column n, as this lane moves it in 16-byte accesses.
 __device__ __forceinline__ void pair_fetch(uint4 (&res)[4], const LinearParams& p, const long long (&row)[4],
                                            const bool (&live)[4], int n, int lane) {
     const char* base = static_cast<const char*>(p.residual) + 16 * (lane & 3);
@@ -319,17 +328,65 @@ __device__ __forceinline__ void pair_fetch(uint4 (&res)[4], const LinearParams& 
         if (live[r]) res[r] = *reinterpret_cast<const uint4*>(base + (row[r] + n) * w);
 }
 
-// One piece from the accumulators of the lane's row to the output.
-template <bool F32>
-__device__ __forceinline__ void pair_piece(const LinearParams& p, const LinearRow& row, int n, const uint32_t* acc,
-                                           const float* s_col, bool any_res, const uint4 (&res)[4], uint4* stage,
-                                           const long long (&out_row)[4], const bool (&live)[4], int lane) {
+// The piece at column n column by column: the residual into the stage (LOAD), or the stage to the
+// output.  Of 16 bits a lane has a column of every row, of fp32 one of every other row.
+template <bool F32, bool LOAD>
+__device__ __forceinline__ void pair_columns(const LinearParams& p, int m0, int n, uint4* stage, int lane) {
+    const int c = F32 ? lane & 15 : lane;
+    const bool in = n + c < p.N;
+    const long long col = LOAD ? (long long)(n + c) : linear_col(p, n + c);
+    int b = m0 / p.tokens, tk = m0 - b * p.tokens;  // the rows' sample and token
+    if (F32 && lane >= 16 && ++tk == p.tokens) tk = 0, ++b;
+    constexpr int R = F32 ? 16 : 32;
+    char* at = reinterpret_cast<char*>(stage) + c % (F32 ? 4 : 8) * (F32 ? 4 : 2);
+    auto place = [&](int i) { return at + 16 * pair_word(F32 ? 2 * i + (lane >> 4) : i, c / (F32 ? 4 : 8)); };
+    uint32_t u[R];  // all read before any is written: the compiler cannot tell the two apart
+    if (!LOAD) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            u[i] = F32 ? *reinterpret_cast<const uint32_t*>(place(i)) : *reinterpret_cast<const uint16_t*>(place(i));
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const bool live = in && m0 + (F32 ? 2 * i + (lane >> 4) : i) < p.M;
+        if (LOAD) {
+            u[i] = 0;
+            if (live) {
+                const long long g = b * p.res_sb + tk * p.res_sn + col;
+                u[i] = F32 ? static_cast<const uint32_t*>(p.residual)[g] : static_cast<const uint16_t*>(p.residual)[g];
+            }
+        } else if (live) {
+            const long long g = b * p.out_sb + tk * p.out_sn + col;
+            if (F32) static_cast<uint32_t*>(p.out)[g] = u[i];
+            else static_cast<uint16_t*>(p.out)[g] = (uint16_t)u[i];
+        }
+        if (++tk == p.tokens) tk = 0, ++b;
+        if (F32 && ++tk == p.tokens) tk = 0, ++b;
+    }
+    if (LOAD) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (F32) *reinterpret_cast<uint32_t*>(place(i)) = u[i];
+            else *reinterpret_cast<uint16_t*>(place(i)) = (uint16_t)u[i];
+        }
+    }
+}
+
+// One piece from the accumulators of the lane's row to the output.  m0: the warp's first row.
+template <bool F32, bool WIDE>
+__device__ __forceinline__ void pair_piece(const LinearParams& p, const LinearRow& row, int m0, int n,
+                                           const uint32_t* acc, const float* s_col, bool any_res, const uint4 (&res)[4],
+                                           uint4* stage, const long long (&out_row)[4], const bool (&live)[4], int lane) {
     constexpr int U = F32 ? 16 : 32;
     float v[U];
-    linear_value<U>(v, p, row, n, acc, s_col, s_col + 256);
+    linear_value<U, WIDE>(v, p, row, n, acc, s_col, s_col + 256);
     if (any_res) {
+        if (WIDE) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) stage[pair_word(8 * r + (lane >> 2), lane & 3)] = res[r];
+            for (int r = 0; r < 4; ++r) stage[pair_word(8 * r + (lane >> 2), lane & 3)] = res[r];
+        } else {
+            pair_columns<F32, true>(p, m0, n, stage, lane);
+        }
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -364,12 +421,16 @@ __device__ __forceinline__ void pair_piece(const LinearParams& p, const LinearRo
         stage[pair_word(lane, j)] = w;
     }
     __syncwarp();
-    const long long col = linear_col(p, n);
-    char* base = static_cast<char*>(p.out) + 16 * (lane & 3);
+    if (WIDE) {
+        const long long col = linear_col(p, n);
+        char* base = static_cast<char*>(p.out) + 16 * (lane & 3);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint4 w = stage[pair_word(8 * r + (lane >> 2), lane & 3)];
-        if (live[r]) *reinterpret_cast<uint4*>(base + (out_row[r] + col) * (F32 ? 4 : 2)) = w;
+        for (int r = 0; r < 4; ++r) {
+            const uint4 w = stage[pair_word(8 * r + (lane >> 2), lane & 3)];
+            if (live[r]) *reinterpret_cast<uint4*>(base + (out_row[r] + col) * (F32 ? 4 : 2)) = w;
+        }
+    } else {
+        pair_columns<F32, false>(p, m0, n, stage, lane);
     }
     __syncwarp();
 }
@@ -522,9 +583,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 res_row[r] = b * p.res_sb + tk * p.res_sn;
             }
             named_bar_sync(1 + half, 128);
-            uint4 res[4];
             const bool any_res = p.vec && p.residual;
-            if (any_res && n0 + 32 <= p.N) pair_fetch(res, p, res_row, live, n0, lane);
+            const int cols = p.out_type == 2 ? 16 : 32;
+            uint4 res[4];  // the residual's piece that comes next
+            auto fetch = [&](int n) {
+                if (any_res && n < n0 + wr && n + cols <= p.N) pair_fetch(res, p, res_row, live, n, lane);
+            };
+            fetch(n0);
             if (!warp_wait_bounded(bar_af(buf), (done >> 1) & 1, abort_flag, lim)) failed = true;
             tc_fence_after();
             const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256 + half * wr;
@@ -535,21 +600,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 tmem_ld32(tl + 32 * ch, acc);
                 tmem_wait_ld();
                 if (failed || n >= p.N) continue;  // the same for the whole warp
+                const int m0 = tm * 256 + rank * 128 + quad * 32;
                 if (p.vec && n + 32 <= p.N) {
-                    const bool more = any_res && 32 * ch + 32 < wr && n + 64 <= p.N;
                     if (p.out_type == 2) {
-                        pair_piece<true>(p, row, n, acc, s_col + 32 * ch, any_res, res, stage, out_row, live, lane);
-                        if (any_res) pair_fetch(res, p, res_row, live, n + 16, lane);
-                        pair_piece<true>(p, row, n + 16, acc + 16, s_col + 32 * ch + 16, any_res, res, stage, out_row,
-                                         live, lane);
+                        pair_piece<true, true>(p, row, m0, n, acc, s_col + 32 * ch, any_res, res, stage, out_row, live,
+                                               lane);
+                        fetch(n + 16);
+                        pair_piece<true, true>(p, row, m0, n + 16, acc + 16, s_col + 32 * ch + 16, any_res, res, stage,
+                                               out_row, live, lane);
                     } else {
-                        pair_piece<false>(p, row, n, acc, s_col + 32 * ch, any_res, res, stage, out_row, live, lane);
+                        pair_piece<false, true>(p, row, m0, n, acc, s_col + 32 * ch, any_res, res, stage, out_row, live,
+                                                lane);
                     }
-                    if (more) pair_fetch(res, p, res_row, live, n + 32, lane);
-                } else if (m < p.M) {
-#pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        if (n + q < p.N) linear_finish1(p, row, n + q, (int)acc[q]);
+                    fetch(n + 32);
+                } else if (p.out_type == 2) {
+                    pair_piece<true, false>(p, row, m0, n, acc, s_col + 32 * ch, p.residual, res, stage, out_row, live,
+                                            lane);
+                    pair_piece<true, false>(p, row, m0, n + 16, acc + 16, s_col + 32 * ch + 16, p.residual, res, stage,
+                                            out_row, live, lane);
+                } else {
+                    pair_piece<false, false>(p, row, m0, n, acc, s_col + 32 * ch, p.residual, res, stage, out_row, live,
+                                             lane);
                 }
                 __syncwarp();
             }
@@ -773,7 +844,7 @@ __global__ void __launch_bounds__(kSplitThreads) int8_split_kernel(const __grid_
             }
             if (whole) {
                 float v[4];
-                linear_value<4>(v, p, row, n, acc, sw, bias);
+                linear_value<4, true>(v, p, row, n, acc, sw, bias);
                 if (row.res) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] += res[q];
