@@ -47,6 +47,7 @@ struct RowParams {
     const void* weight;        // [C] each, or NULL
     const void* bias;
     const void* post_weight;
+    const char *x_end, *y_end;  // past the last byte of x and y (rows off the 16-byte grid)
     long long x_sb, x_sn, y_sb, y_sn, r_sb, r_sn, h_sb, h_sn;  // strides in elements
     long long x_sh;            // x in head layout: channel c is channel c % D of head c / D
     int D;                     // head dimension; 0 = plain rows
@@ -141,25 +142,62 @@ __device__ __forceinline__ Raw8<T> row_edge(const char* base, int c, int C) {
     if (T == kRowFp32) r.w[Raw8<T>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
     return r;
 }
+// Zeros for the values outside the row.
+template <int T>
+__device__ __forceinline__ void row_mask(Raw8<T>& r, int c, int C) {
+    uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, 0, 0, 0, 0};
+    if (T == kRowFp32) {
+        const uint4 b = r.w[Raw8<T>::kWords - 1];
+        u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool in = (unsigned)(c + e) < (unsigned)C;
+        if (T == kRowFp32) u[e] = in ? u[e] : 0u;
+        else u[e / 2] &= in ? 0xffffffffu : e & 1 ? 0x0000ffffu : 0xffff0000u;
+    }
+    r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    if (T == kRowFp32) r.w[Raw8<T>::kWords - 1] = make_uint4(u[4], u[5], u[6], u[7]);
+}
+// [lo, hi): the bytes of the whole tensor.  A row's first and last 16 bytes may hold its
+// neighbours' values, which are read too and masked later; nothing outside the tensor is
+// read.  (Its own two ends, and a tensor that starts elsewhere on the 16-byte grid than the chunks
+// do, go value by value, in little code.)
 template <int T, bool VEC>
-__device__ __forceinline__ void row_load(Raw8<T>& raw, const char* base, int v, const RowPlace& q) {
+__device__ __forceinline__ void row_load(Raw8<T>& raw, const char* base, int v, const RowPlace& q, const char* lo,
+                                         const char* hi) {
     constexpr int W = T == kRowFp32 ? 4 : 2;
     const int c = row_col<VEC>(v, q);
     const char* p = base + c * W;
-    if (row_full<VEC>(v, q) && (VEC || on16(p))) {
+    if (VEC ? v < q.live : c < q.C && p >= lo && p + 8 * W <= hi && on16(p)) {
 #pragma unroll
         for (int i = 0; i < Raw8<T>::kWords; ++i) raw.w[i] = ldg_stream(p + 16 * i);
-    } else if (!VEC && c < q.C) {
-        raw = row_edge<T>(base, c, q.C);
     } else {
 #pragma unroll
         for (int i = 0; i < Raw8<T>::kWords; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
+        if (!VEC && c < q.C) {
+#pragma unroll 1
+            for (int e = 7; e >= 0; --e) {
+                const bool in = (unsigned)(c + e) < (unsigned)q.C;
+                uint4 &a = raw.w[0], &b = raw.w[Raw8<T>::kWords - 1];
+                if (T == kRowFp32) {
+                    b.w = b.z; b.z = b.y; b.y = b.x; b.x = a.w; a.w = a.z; a.z = a.y; a.y = a.x;
+                    a.x = in ? reinterpret_cast<const uint32_t*>(base)[c + e] : 0u;
+                } else {
+                    a.w = a.w << 16 | a.z >> 16;
+                    a.z = a.z << 16 | a.y >> 16;
+                    a.y = a.y << 16 | a.x >> 16;
+                    a.x = a.x << 16 | (in ? reinterpret_cast<const uint16_t*>(base)[c + e] : 0u);
+                }
+            }
+        }
     }
 }
 
 // As four packed pairs of floats.
-template <int T>
-__device__ __forceinline__ void row_values(const Raw8<T>& raw, uint64_t (&f)[4]) {
+template <int T, bool VEC>
+__device__ __forceinline__ void row_values(Raw8<T>& raw, uint64_t (&f)[4], int v, const RowPlace& q) {
+    if (!VEC && !row_full<VEC>(v, q)) row_mask<T>(raw, row_col<VEC>(v, q), q.C);
     const uint4 a = raw.w[0], b = raw.w[Raw8<T>::kWords - 1];
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -228,11 +266,11 @@ __device__ __forceinline__ void param_load(uint64_t (&f)[4], const char* base, i
         const char* p = base + (c - s) * PW;
         if (!inside) {
             if (param32) {
-                const Raw8<kRowFp32> r = row_edge<kRowFp32>(base, c, q.C);
-                row_values<kRowFp32>(r, f);
+                Raw8<kRowFp32> r = row_edge<kRowFp32>(base, c, q.C);
+                row_values<kRowFp32, true>(r, f, v, q);
             } else {
-                const Raw8<T16 == kRowFp32 ? kRowBf16 : T16> r = row_edge<T16 == kRowFp32 ? kRowBf16 : T16>(base, c, q.C);
-                row_values<T16 == kRowFp32 ? kRowBf16 : T16>(r, f);
+                Raw8<T16 == kRowFp32 ? kRowBf16 : T16> r = row_edge<T16 == kRowFp32 ? kRowBf16 : T16>(base, c, q.C);
+                row_values<T16 == kRowFp32 ? kRowBf16 : T16, true>(r, f, v, q);
             }
             return;
         }
@@ -457,11 +495,11 @@ __global__ void __launch_bounds__(WARP                  ? 128
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             if (!heads) {
-                row_load<XT, VEC>(rx[v], a.x, v, qa);
+                row_load<XT, VEC>(rx[v], a.x, v, qa, static_cast<const char*>(p.x), p.x_end);
             } else if (VEC) {
                 const int hd = row_col<true>(v, q) / p.D;
                 // the head's row, moved back so that column c of it is channel c % D
-                row_load<XT, VEC>(rx[v], a.x + hd * (p.x_sh - p.D) * XW, v, qa);
+                row_load<XT, VEC>(rx[v], a.x + hd * (p.x_sh - p.D) * XW, v, qa, nullptr, nullptr);
             } else {
                 const int c = row_col<true>(v, q);
                 uint32_t u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -478,7 +516,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
         }
         if (has_y) {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_load<HT, VEC>(ry[v], a.y, v, qa);
+            for (int v = 0; v < VPT; ++v) row_load<HT, VEC>(ry[v], a.y, v, qa, static_cast<const char*>(p.y), p.y_end);
         }
     };
 
@@ -524,7 +562,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
         if (has_y) {
             uint64_t z[VPT][4];
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_values<HT>(ry[v], z[v]);
+            for (int v = 0; v < VPT; ++v) row_values<HT, VEC>(ry[v], z[v], v, q);
             float inv = 1.f;
             if (has_post) inv = row_statistics<WARP, VPT, VEC>(z, p.post == kNormLayer, q, inv_c, p.eps, red, slot);
             if (has_post) {
@@ -537,7 +575,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
                 if (p.post_weight) row_step<kStepMul, HT, VPT, VEC>(z, z, static_cast<const char*>(p.post_weight), param32, q);
             }
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_values<XT>(rx[v], f[v]);
+            for (int v = 0; v < VPT; ++v) row_values<XT, VEC>(rx[v], f[v], v, q);
             if (has_gate) {
                 row_step<kStepGate, HT, VPT, VEC>(f, z, static_cast<const char*>(p.gate) + goff, param32, q);
             } else {
@@ -551,7 +589,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
             for (int v = 0; v < VPT; ++v) row_store<XT, VEC>(at.r, f[v], v, q);
         } else {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) row_values<XT>(rx[v], f[v]);
+            for (int v = 0; v < VPT; ++v) row_values<XT, VEC>(rx[v], f[v], v, q);
         }
 
         // the next row's loads run under this one's statistics and stores

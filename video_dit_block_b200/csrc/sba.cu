@@ -981,6 +981,8 @@ extern "C" sba_status sba_residual_norm(const void* x, const void* y, void* x_ou
     p.r_sb = strides[4]; p.r_sn = strides[5]; p.h_sb = strides[6]; p.h_sn = strides[7];
     p.N = N; p.C = C; p.G = G;
     p.rows = (long long)B * N;
+    p.x_end = static_cast<const char*>(x) + ((B - 1) * strides[0] + (N - 1) * strides[1] + C) * xw;
+    if (y) p.y_end = static_cast<const char*>(y) + ((B - 1) * strides[2] + (N - 1) * strides[3] + C) * hw;
     p.norm = norm; p.post = post_norm; p.quant = out_scale != nullptr;
     p.Cq = (C + 15) / 16 * 16;
     if (p.quant && (p.h_sb % 16 || p.h_sn % 16)) return SBA_ERR_ALIGNMENT;
@@ -1005,6 +1007,7 @@ extern "C" sba_status sba_token_quantize(const void* x, int dtype, int B, int H,
     std::memset(&p, 0, sizeof(p));
     p.x = x; p.h = codes; p.h_scale = scales;
     p.x_sb = strides[0]; p.x_sh = strides[1]; p.x_sn = strides[2];
+    p.x_end = static_cast<const char*>(x) + ((B - 1) * strides[0] + (N - 1) * strides[2] + D) * w;  // of plain rows
     p.D = H > 1 ? D : 0;
     p.N = N; p.C = H * D; p.G = 1;
     p.Cq = (p.C + 15) / 16 * 16;
