@@ -1088,7 +1088,10 @@ extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, con
     while (p.stages > 2 && (SM::alloc(p.bn, p.box_rows, p.stages) + 1024) * per_sm > 227 * 1024) --p.stages;
     const int smem = SM::alloc(p.bn, p.box_rows, p.stages);
     if (!make_map_codes(&ta, a, p.M, K, p.box_rows) || !make_map_codes(&tw, w, M, K, p.bn)) return SBA_ERR_CUDA;
-    if (cudaFuncSetAttribute(sba::int8_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // the same limit for every size: a smaller one could come between another thread's limit and
+    // its launch
+    if (cudaFuncSetAttribute(sba::int8_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+        cudaSuccess)
         return SBA_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));

@@ -8,7 +8,6 @@ CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -486,7 +485,7 @@ _LAYOUTS = {"interleaved": 0, "half": 1}
 _Strides3, _Strides5, _Strides6, _Strides8 = (ctypes.c_int64 * n for n in (3, 5, 6, 8))
 
 
-def _place(device, stream):
+def _elsewhere(device, stream):
     """The context of a call on GPU `device` (its index): allocations and launch on `stream`, or
     on the device's current stream.  None when that is where the caller is already."""
     if device < 0:
@@ -498,21 +497,9 @@ def _place(device, stream):
     return torch.cuda.stream(stream)
 
 
-def _on_device(call):
-    """Runs an operator where its first tensor lives, on the `stream` that it is given."""
-    @functools.wraps(call)
-    def placed(x, *args, stream=None, **kwargs):
-        where = _place(x.get_device(), stream)
-        if where is None:
-            return call(x, *args, **kwargs)
-        with where:
-            return call(x, *args, **kwargs)
-    return placed
-
-
 def _values(t, name, shape, device, dtype):
     """Check an optional tensor: shape, device, type, contiguous."""
-    if t is not None and (t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous()):
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device):
         raise ValueError(f"{name}: expected a contiguous {tuple(shape)} tensor of {dtype} on cuda:{device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
 
@@ -520,7 +507,7 @@ def _values(t, name, shape, device, dtype):
 def _rows(t, name, shape, device, dtype, written=False):
     """Check rows at any strides: the last dimension contiguous, and no two elements of a
     written tensor in one place."""
-    if t.get_device() != device or t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{device}, got {tuple(t.shape)} {t.dtype} on "
                          f"{t.device}")
     if t.is_contiguous():
@@ -568,10 +555,9 @@ def _tables(tables, C, index, rows, dtype, device, kind=None):
     return G, _params(tables, (G, C), dtype, device, kind)
 
 
-@_on_device
 def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, scale=None, shift=None, index=None,
                   post_norm=None, post_weight=None, valid_len=None, eps: float = 1e-6, quantize: bool = False,
-                  out_dtype=None, x_out=None, out=None, out_scale=None):
+                  out_dtype=None, x_out=None, out=None, out_scale=None, stream=None):
     """The gated residual of a block's output y, and the modulated norm of the new residual
     stream, in one pass (see include/sba.h).
 
@@ -588,6 +574,11 @@ def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, sc
     quantize=True returns (r, codes, scales) for int8_linear: int8 [B, N, C rounded up to
     16] and fp32 [B, N].  h has y's type (out_dtype without a y, x's by default).  x_out
     may be x, out may be y."""
+    where = _elsewhere(x.get_device(), stream)
+    if where is not None:
+        with where:
+            return residual_norm(x, y, gate, norm, weight, bias, scale, shift, index, post_norm, post_weight, valid_len,
+                                 eps, quantize, out_dtype, x_out, out, out_scale)
     shape, dev, xtype = x.shape, x.get_device(), x.dtype
     if len(shape) != 3 or xtype not in _DTYPES:
         raise ValueError("x: expected [B, N, C] in bf16, fp16 or fp32")
@@ -605,8 +596,11 @@ def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, sc
     ptype = None
     if weight is not None or bias is not None or post_weight is not None:
         ptype = _params((("weight", weight), ("bias", bias), ("post_weight", post_weight)), (C,), dtype, dev)
-    G, ptype = _tables((("gate", gate), ("scale", scale), ("shift", shift)), C, index, (B, N), dtype, dev, ptype)
-    _values(valid_len, "valid_len", (B,), dev, torch.int32)
+    G = 0
+    if gate is not None or scale is not None or shift is not None or index is not None:
+        G, ptype = _tables((("gate", gate), ("scale", scale), ("shift", shift)), C, index, (B, N), dtype, dev, ptype)
+    if valid_len is not None:
+        _values(valid_len, "valid_len", (B,), dev, torch.int32)
     strides = [x.stride(0), x.stride(1), 0, 0, 0, 0, 0, 0]
     if y is not None:
         _rows(y, "y", shape, dev, dtype)
@@ -645,13 +639,17 @@ def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, sc
     return (r, out, out_scale) if quantize else (r, out)
 
 
-@_on_device
-def token_quantize(x, codes=None, scales=None):
+def token_quantize(x, codes=None, scales=None, stream=None):
     """Rows in 8 bits with one scale a row: scales = max|row| / 127, codes the nearest integers
     (see include/sba.h).  x: [..., K] of bf16, fp16 or fp32, [M, K] (tokens, or a weight's
     output channels), [B, N, K], or the attention's head layout [B, H, N, D], whose K = H * D;
     at any strides with contiguous rows.  Returns (codes int8 [M, K'] or [B, N, K'], scales
     fp32 [M] or [B, N]), K' = K rounded up to a multiple of 16 (zero codes)."""
+    dev = x.get_device()
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return token_quantize(x, codes, scales)
     shape, strides = x.shape, x.stride()
     kind = _DTYPES.get(x.dtype)
     if kind is None or not 2 <= len(shape) <= 4 or (strides[-1] != 1 and shape[-1] > 1):
@@ -670,20 +668,19 @@ def token_quantize(x, codes=None, scales=None):
     if codes is None:
         codes = x.new_empty((*lead, width), dtype=torch.int8)
     else:
-        _values(codes, "codes", (*lead, width), x.get_device(), torch.int8)
+        _values(codes, "codes", (*lead, width), dev, torch.int8)
     if scales is None:
         scales = x.new_empty(lead, dtype=torch.float32)
     else:
-        _values(scales, "scales", lead, x.get_device(), torch.float32)
+        _values(scales, "scales", lead, dev, torch.float32)
     if B and N:
         _check(lib().sba_token_quantize(x.data_ptr(), kind, B, H, N, D, _Strides3(sb, sh, sn), codes.data_ptr(),
-                                        scales.data_ptr(), torch._C._cuda_getCurrentRawStream(x.get_device())), "sba_token_quantize")
+                                        scales.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)), "sba_token_quantize")
     return codes, scales
 
 
-@_on_device
 def int8_linear(codes, scales, weight_codes, weight_scales, bias=None, activation=None, gate=None, index=None,
-                residual=None, out_dtype=torch.bfloat16, heads=None, out=None):
+                residual=None, out_dtype=torch.bfloat16, heads=None, out=None, stream=None):
     """A projection in 8-bit integers with its epilogue (see include/sba.h):
 
       out = residual + gate * activation((codes @ weight_codes.T) * scales * weight_scales + bias)
@@ -695,6 +692,11 @@ def int8_linear(codes, scales, weight_codes, weight_scales, bias=None, activatio
     residual: of out's shape and type, contiguous rows, may be out.  Returns out [..., M]; with
     heads=H (and codes [B, N, K]) the attention's layout [B, H, N, M / H] instead."""
     shape, dev = codes.shape, codes.get_device()
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return int8_linear(codes, scales, weight_codes, weight_scales, bias, activation, gate, index, residual,
+                               out_dtype, heads, out)
     if len(shape) == 3:
         B, N, K = shape
         lead = (B, N)
@@ -800,8 +802,7 @@ def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scalin
     return RopeTable(freq * axes, [a for a in range(axes) for _ in range(d // 2)], amplitude)
 
 
-@_on_device
-def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool = False, out=None):
+def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool = False, out=None, stream=None):
     """Rotary positions (see include/sba.h): the first table.rope_dim channels of x [B, H, N, D]
     turned by the token's position, the others copied.  x: bf16, fp16 or fp32 at any strides
     with contiguous channels (a token-major [B, N, H, D] tensor is x.transpose(1, 2)).  pos:
@@ -809,6 +810,10 @@ def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool 
     "interleaved", or (p, p + rope_dim / 2), "half".  inverse turns back, which is also the
     gradient.  out may be x.  Returns out (laid out as x)."""
     shape, dev, strides = x.shape, x.get_device(), x.stride()
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return rotary(x, pos, table, layout, inverse, out)
     dtype = _DTYPES.get(x.dtype)
     if len(shape) != 4 or dtype is None:
         raise ValueError("x: expected [B, H, N, D] in bf16, fp16 or fp32")
