@@ -6,7 +6,7 @@ sba_pair_query_blocks (which two query blocks share an attention tile) and
 sba_attention_paired over the kept blocks.  Prints ONE JSON line (rank 0).
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--config NAME] [--impl ours|reference]
-                  [--router mean|lse] [--budget B] [--producer] [--compensate first|mean]
+                  [--router mean|lse] [--budget B] [--producer] [--compensate first|mean] [--projections]
 
 The default workload is long_clip (B 2, H 32, D 128, a 31x34x60 latent grid with 15% of
 the tokens pruned per sample, ragged lengths, sparsity 0.75): the largest of the five
@@ -21,7 +21,13 @@ from those means (sba_pool_select_means) and attends over the normalised Q and K
 `--compensate first` attends with the first-order compensation of the dropped blocks
 (sba_attention_compensated, which walks every block), `--compensate mean` with the
 mean-key form (sba_attention_mean_compensated); the metric still counts kept-block
-FLOPs only.
+FLOPs only.  `--projections` times the whole attention sub-block, from the residual
+stream [B, Npad, H*D] back onto it: modulated norm in 8 bits (sba_residual_norm), the
+query, key and value projections into the head layout (sba_int8_linear), the step
+above, its output in 8 bits (sba_token_quantize), the output projection gated onto
+the stream, and the modulated norm of the new stream in 8 bits, which the
+feed-forward would read; random-init projections, Q and K as the projections give
+them (or through --producer).
 
 The line carries a `parity` object: for two heads of the timed workload, the GPU's
 routing against the oracle's (rows checked, rows that differ, rows excused as score
@@ -76,9 +82,15 @@ def parse():
     ap.add_argument("--prune", type=float, default=None, metavar="RATIO",
                     help="prune each sample to RATIO of its tokens by feature-norm saliency at the start of "
                          "every step (token features of width H*D), then gather Q, K, V")
+    ap.add_argument("--projections", action="store_true",
+                    help="start each step at the residual stream (width H*D) and end it there: modulated norm, 8-bit "
+                         "projections around the attention, gated residual, norm (not with --prune)")
     ap.add_argument("--attn-kernel", default="auto", choices=["auto", "query_pairs", "cta_pair"],
                     help="D = 128 attention kernel: the default query pairs, or the opt-in CTA pair")
-    return ap.parse_args()
+    args = ap.parse_args()
+    if args.projections and args.prune is not None:
+        ap.error("--projections and --prune: choose one")
+    return args
 
 
 # DRAM traffic (dram__bytes_read.sum + dram__bytes_write.sum) of one attention launch,
@@ -453,9 +465,28 @@ def run_ours(args):
     pair_order = torch.empty((B, H, 2 * ((nQ + 1) // 2)), dtype=torch.int32, device=dev)
     pws = torch.empty(int(sba.lib().sba_pair_workspace_size(B, H, Npad, 64)), dtype=torch.uint8, device=dev)
 
+    if args.projections:
+        C = H * D
+        g = torch.Generator(device=dev)
+        g.manual_seed(20261202)
+        rand = lambda *shape, std=1.0: torch.randn(shape, generator=g, device=dev) * std
+        hidden = rand(B, Npad, C).to(torch.bfloat16)
+        gate, scale, shift = (rand(B, C, std=0.3) for _ in range(3))
+        proj = [sba.token_quantize(rand(C, C, std=C ** -0.5)) for _ in range(4)]  # query, key, value, output
+        h_codes = torch.empty((B, Npad, C), dtype=torch.int8, device=dev)
+        h_scale = torch.empty((B, Npad), dtype=torch.float32, device=dev)
+        stream_out = torch.empty_like(hidden)
+
     def prep(qq=q, kk=k, vv=v, vll=vl, xx=None):
         """With --prune: saliency pruning of the step's tokens, then the compacted Q, K, V
-        and valid lengths; otherwise the inputs as they are."""
+        and valid lengths.  With --projections: Q, K, V from the residual stream.  Otherwise
+        the inputs as they are."""
+        if args.projections:
+            sba.residual_norm(hidden, scale=scale, shift=shift, valid_len=vll, quantize=True, out=h_codes,
+                              out_scale=h_scale, stream=stream)
+            for dst, (wc, wsc) in zip((qq, kk, vv), proj):
+                sba.int8_linear(h_codes, h_scale, wc, wsc, heads=H, out=dst, stream=stream)
+            return qq, kk, vv, vll
         if args.prune is None:
             return qq, kk, vv, vll
         sba.token_prune(x if xx is None else xx, vll, args.prune, npad_out=Npad, idx=pr_idx, valid_out=pr_vl,
@@ -512,6 +543,12 @@ def run_ours(args):
                                            lse=lse, workspace=cws, stream=stream)
         else:
             sba.attention_paired(qq, kk, vv, kv_idx, kv_cnt, pair_order, vll, out=out, lse=lse, stream=stream)
+        if args.projections:
+            # the output projection gated onto the stream, and the next sub-block's norm
+            sba.token_quantize(out, codes=h_codes, scales=h_scale, stream=stream)
+            sba.int8_linear(h_codes, h_scale, *proj[3], gate=gate, residual=hidden, out=stream_out, stream=stream)
+            sba.residual_norm(stream_out, scale=scale, shift=shift, valid_len=vll, quantize=True, out=h_codes,
+                              out_scale=h_scale, stream=stream)
 
     def step(qq=q, kk=k, vv=v, vll=vl, xx=None):
         qq, kk, vv, vll = prep(qq, kk, vv, vll, xx)
@@ -620,7 +657,7 @@ def run_ours(args):
     # download overlap step i's compute.  Timed from the first upload to the last
     # download.
     e2e = None
-    if not args.no_e2e:
+    if not args.no_e2e and not args.projections:  # (its inputs are made on the device)
         qh, kh, vh = (z.cpu().pin_memory() for z in (q, k, v))
         vlh = vl.cpu().pin_memory()
         xh = x.cpu().pin_memory() if args.prune is not None else None
@@ -685,7 +722,8 @@ def run_ours(args):
         "metric": METRIC, "value": value, "unit": "TFLOP/s", "n_gpus": world, "steps": K,
         "warmup": args.warmup, "ms_per_step": ms_step, "higher_is_better": True, "scaling": "weak",
         "vs_baseline": None, "dtype": "bf16",
-        "data": "synthetic (seeded smooth field + noise, bf16; no weights involved)",
+        "data": "synthetic (seeded normal residual stream, bf16; random-init 8-bit projections)" if args.projections
+                else "synthetic (seeded smooth field + noise, bf16; no weights involved)",
         "config": workload_config(w, {
             "l2": f"inputs {3 * q.numel() * 2 / 1e6:.0f} MB > 126 MB L2; no flush between steps "
                   "(median_ms.l2_flushed: a 512 MB write before each of its rounds)",
@@ -719,9 +757,11 @@ def run_ours(args):
         # (--producer: 2 producer launches and 2 splits of the given means replace pooling)
         # (--compensate mean: 2 block-mean launches before the attention)
         # (--prune: norm + select + 3 gathers, and the positions' gather with --producer)
+        # (--projections: norm, 3 products, the output's codes, 1 product, norm)
         "gpu_launches": ((3 + (1 if w.sparsity > 0 else 0) if lse_router else 5) + (3 if args.producer else 0)
                          + (0 if pair_kernel else 3) + 1 + (2 if args.compensate == "mean" else 0)
-                         + (5 + (1 if args.producer else 0) if args.prune is not None else 0)) * K,
+                         + (5 + (1 if args.producer else 0) if args.prune is not None else 0)
+                         + (7 if args.projections else 0)) * K,
         "clocks": clk,
     }
     if not lse_router and not args.producer:
@@ -739,8 +779,15 @@ def run_ours(args):
                                      "valid_len_after": [int(z) for z in vl_step], "Npad_after": Npad}
         # the norm kernel reads the features once: its share of the pruning stage's time
         line["prune_feature_gbs"] = x.numel() * 2 / (prune_ms * 1e-3) / 1e9
+    if args.projections:
+        line["config"]["projections"] = f"8-bit integer, [{C}, {C}] x 4, around the attention; attn_ms includes the " \
+                                        "output projection and the norm after it, select_ms those before"
     if par_data is not None:
         pw = w
+        if args.projections:
+            import copy
+            pw = copy.copy(w)  # the oracle gets the projections' own outputs
+            pw.q, pw.k, pw.v = (z.view(torch.int16).cpu().numpy().view(np.uint16) for z in (q, k, v))
         if args.prune is not None:
             import oracle
             io, vo, _ = oracle.token_prune(xf_host, w.valid_len, args.prune, npad_out=Npad)
