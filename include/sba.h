@@ -351,9 +351,10 @@ sba_status sba_gather_tokens(const void* src, int B, int H, int N, int row_bytes
  * 0 only where an input is broadcast.  Pointers need the alignment of their element only
  * (16 bytes for int8 codes); rows whose addresses are all multiples of 16 bytes run
  * faster.  An output may be the input of the same shape, type and strides named below as
- * allowed; otherwise outputs overlap nothing.  Statistics, sums and products are in fp32
- * (the integer sums exact) and each output is rounded once, to nearest even.  An index
- * outside its table raises SBA_ERR_DEVICE_FLAG and reads row 0. */
+ * allowed (at an input's address otherwise: SBA_ERR_INVALID_ARG); outputs overlap
+ * nothing else.  Statistics, sums and products are in fp32 (the integer sums exact) and
+ * each output is rounded once, to nearest even.  An index outside its table raises
+ * SBA_ERR_DEVICE_FLAG and reads row 0. */
 typedef enum { SBA_DTYPE_BF16 = 0, SBA_DTYPE_FP16 = 1, SBA_DTYPE_FP32 = 2 } sba_dtype;
 
 #define SBA_NORM_NONE 0
@@ -372,7 +373,8 @@ typedef enum { SBA_DTYPE_BF16 = 0, SBA_DTYPE_FP16 = 1, SBA_DTYPE_FP32 = 2 } sba_
  *   h = (norm(r) * weight + bias) * (1 + scale[g]) + shift[g]
  * and, with out_scale given, h in 8 bits: out_scale = max|h| / 127 and
  * code = nearest integer (ties to even) to fp32(h * fp32(127 / max|h|)); a row with
- * max|h| < 2^-100 gets codes and scale 0.
+ * max|h| < 2^-100 gets codes and scale 0.  A row with a NaN, or else an infinity, gets
+ * that as its scale (its codes mean nothing), so that it shows in every product.
  *   x            [B, N, C] of x_dtype: the residual stream
  *   y            [B, N, C] of dtype, or NULL
  *   x_out        [B, N, C] of x_dtype (written): r.  Required with y, unused without;

@@ -92,6 +92,42 @@ def test_rotary_rejects(lib, kw, code):
                           a["amp"], 0, None) == code
 
 
+P, Q, R = (ctypes.c_void_p(n) for n in (0x20000, 0x30000, 0x40000))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=A, y=P, r=Q, h=Q),                                            # both outputs in one place
+    dict(x=A, y=P, r=P, h=Q),                                            # the residual stream over the block's output
+    dict(x=A, y=P, r=A, h=Q, st=[512, 64, 512, 64, 1024, 64, 512, 64]),  # in place, other strides
+    dict(x=A, y=P, r=A, h=Q, st=[64, 128, 512, 64, 64, 256, 512, 64]),
+    dict(x=A, y=P, r=Q, h=P, st=[512, 64, 512, 64, 512, 64, 512, 128]),
+    dict(x=A, y=P, r=Q, h=P, hs=R), dict(x=A, y=None, r=None, h=A, hs=R),
+    dict(x=A, y=None, r=None, h=A, xt=FP32),
+])
+def test_residual_norm_rejects_overlaps(lib, kw):
+    assert norm(lib, **kw) == 1
+
+
+def test_others_reject_overlaps(lib):
+    for heads, st in ((2, [512, 64, 512, 64, 64]), (0, [512, 64, 1024, 0, 64]), (0, [512, 64, 512, 0, 128])):
+        assert lib.sba_int8_linear(A, P, A, P, 2, 8, 64, 64, None, None, FP32, 0, None, 0, Q, Q, BF16, heads, i64(*st),
+                                   None) == 1
+    for w, out in ((A, P), (P, A)):
+        assert lib.sba_int8_linear(w, Q, out, Q, 2, 8, 64, 64, None, None, FP32, 0, None, 0, None, A, BF16, 0,
+                                   i64(0, 0, 512, 0, 64), None) == 1
+    assert lib.sba_token_quantize(A, BF16, 1, 1, 8, 64, i64(512, 0, 64), A, P, None) == 1
+    f, a = (ctypes.c_double * 32)(*[1.0] * 32), (ctypes.c_uint8 * 32)()
+    for st in ([0, 1024, 128, 0, 1024, 256], [0, 1024, 128, 0, 128, 128]):
+        assert lib.sba_rotary(A, A, BF16, P, 1, 1, 2, 8, 128, i64(*st), 64, 0, f, a, 1.0, 0, None) == 1
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    from video_dit_block_b200 import sba
+    sba._counts(1, 0x7fffffff)
+    with pytest.raises(ValueError):
+        sba._counts(1, 0x80000000)
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
 

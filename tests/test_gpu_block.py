@@ -423,6 +423,39 @@ def test_token_quantize_hard_rows(sba):
     assert not codes[3].any() and scales[3] == 0
 
 
+@pytest.mark.parametrize("shape", [(7, 40), (7, 333), (7, 1024), (7, 5120), (7, 5121), (7, 20480), (2, 3, 5, 64)])
+@pytest.mark.parametrize("dt", [BF, SF])
+def test_token_quantize_shows_nan_and_infinities(sba, shape, dt):
+    """They become the row's scale, and the other rows stay as they are."""
+    g = gen(23)
+    x = randn(g, *shape, dtype=dt)
+    rows = x.transpose(1, 2).flatten(2).flatten(0, 1) if x.dim() == 4 else x
+    ref, sref = codes_ref(rows)
+    N = 5 if x.dim() == 4 else 7
+
+    def put(i, c, v):
+        if x.dim() == 4:
+            x[i // N, c // 64, i % N, c % 64] = v
+        else:
+            x[i, c] = v
+
+    K = rows.shape[1]
+    put(1, K - 1, float("nan"))
+    put(2, 0, float("inf"))
+    put(3, K // 2, float("-inf"))
+    put(5, 3, float("nan"))
+    put(5, K // 2, float("inf"))
+    codes, scales = sba.token_quantize(x)
+    codes, scales = codes.flatten(0, -2), scales.flatten()
+    assert scales[[1, 5]].isnan().all() and (scales[[2, 3]] == float("inf")).all()
+    for i in (0, 4, 6):
+        np.testing.assert_array_equal(codes[i, :K].cpu().numpy(), ref[i])
+        assert scales[i].item() == sref[i]
+    w, ws = sba.token_quantize(randn(g, 32, K))
+    y = sba.int8_linear(codes, scales, w, ws)
+    assert not y[[1, 2, 3, 5]].isfinite().any() and y[[0, 4, 6]].isfinite().all()
+
+
 def test_token_quantize_strides(sba):
     g = gen(22)
     x = randn(g, 2, 5, 3, 3 * 64, dtype=BF)

@@ -301,11 +301,18 @@ __device__ __forceinline__ void param_load(uint64_t (&f)[4], const char* base, i
     for (int i = 0; i < 4; ++i) f[i] = pack2(g[2 * i], g[2 * i + 1]);
 }
 
+// The larger of two values; a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Sum or maximum over the threads of a row: a warp's, or a CTA's.  `slot` alternates between
 // calls, so one barrier per reduction suffices.
 template <bool WARP, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float (*red)[32], int& slot) {
-    if (MAX) {  // of values that are not negative: their bits are in their order
+    if (MAX) {  // of values that are not negative: their bits are in their order, a NaN above all
         v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
     } else {
 #pragma unroll
@@ -318,9 +325,10 @@ __device__ __forceinline__ float row_reduce(float v, float (*red)[32], int& slot
         const float4* r = reinterpret_cast<const float4*>(red[slot]);
         for (int i = 0; i < (int)blockDim.x; i += 256) {  // eight warps
             const float4 a = r[i / 128], b = r[i / 128 + 1];
-            const float w = MAX ? fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)))
+            const float w = MAX ? max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)),
+                                          max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)))
                                 : ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
-            v = i == 0 ? w : MAX ? fmaxf(v, w) : v + w;
+            v = i == 0 ? w : MAX ? max_nan(v, w) : v + w;
         }
         slot ^= 1;
     }
@@ -645,7 +653,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
             continue;
         }
 
-        // columns past C hold 0
+        // columns past C hold 0; a NaN becomes the row's scale
         float top = 0.f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
@@ -653,12 +661,12 @@ __global__ void __launch_bounds__(WARP                  ? 128
             for (int i = 0; i < 4; ++i) {
                 float lo, hi;
                 unpack2(f[v][i], lo, hi);
-                asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(lo), "f"(hi));
+                asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(lo), "f"(hi));
             }
         }
         top = row_reduce<WARP, true>(top, red, slot);
         // below 2^-100 the reciprocal step would leave fp32's range: such a row counts as zero
-        const bool zero = !(top >= 7.888609052210118e-31f);
+        const bool zero = top < 7.888609052210118e-31f;
         const float inv = zero ? 0.f : __fdiv_rn(127.f, top);
         if (t == 0) p.h_scale[at.row] = zero ? 0.f : __fdiv_rn(top, 127.f);
         // Adding 1.5 * 2^23 to a product of at most 127 rounds it to the nearest integer, ties to

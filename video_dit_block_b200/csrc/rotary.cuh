@@ -95,8 +95,9 @@ __global__ void __launch_bounds__(256, 3) rotary_vec_kernel(const __grid_constan
     constexpr int U = F32 ? 2 : 4;  // heads in flight
     const int tpt = p.D >> 4;       // threads per token
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int n = (int)(id / tpt), j = (int)(id % tpt);
-    if (n >= p.N) return;
+    const int j = (int)(id % tpt);
+    if (id / tpt >= p.N) return;
+    const int n = (int)(id / tpt);
     const int b = blockIdx.z;
     const int h0 = blockIdx.y * p.heads_per_cta;
     const int h1 = min(p.H, h0 + p.heads_per_cta);

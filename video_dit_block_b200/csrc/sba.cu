@@ -803,6 +803,12 @@ bool none_negative(const int64_t* s, int n) {
     return true;
 }
 
+// Whether an output may start at an input's address: the rows at the same places (strides of
+// sample, token).
+bool in_place(const void* in, const int64_t* si, const void* out, const int64_t* so, int B, int N, bool same_type) {
+    return in != out || (same_type && (B == 1 || si[0] == so[0]) && (N == 1 || si[1] == so[1]));
+}
+
 template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32 = true>
 sba_status launch_rows(const sba::RowParams& p, int chunks, cudaStream_t s) {
     const auto kernel = sba::residual_norm_kernel<XT, HT, WARP, VPT, VEC, KIND, P32>;
@@ -986,6 +992,10 @@ extern "C" sba_status sba_residual_norm(const void* x, const void* y, void* x_ou
     p.norm = norm; p.post = post_norm; p.quant = out_scale != nullptr;
     p.Cq = (C + 15) / 16 * 16;
     if (p.quant && (p.h_sb % 16 || p.h_sn % 16)) return SBA_ERR_ALIGNMENT;
+    if (y && (x_out == y || !in_place(x, strides, x_out, strides + 4, B, N, true))) return SBA_ERR_INVALID_ARG;
+    if (norm && (out == x_out || !in_place(x, strides, out, strides + 6, B, N, !p.quant && x_dtype == dtype) ||
+                 !in_place(y, strides + 2, out, strides + 6, B, N, !p.quant)))
+        return SBA_ERR_INVALID_ARG;
     p.param32 = param_dtype == SBA_DTYPE_FP32;
     p.eps = eps;
     const bool vec = C % 8 == 0 && rows16(x, strides, 2, xw) && (!y || (rows16(y, strides + 2, 2, hw) &&
@@ -1003,6 +1013,7 @@ extern "C" sba_status sba_token_quantize(const void* x, int dtype, int B, int H,
     if ((long long)H * D > SBA_MAX_CHANNELS || (long long)B * N > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
     const int w = dtype_bytes(dtype);
     if (!aligned_to(x, w) || !aligned16(codes) || !aligned_to(scales, 4)) return SBA_ERR_ALIGNMENT;
+    if (static_cast<const void*>(codes) == x) return SBA_ERR_INVALID_ARG;
     sba::RowParams p;
     std::memset(&p, 0, sizeof(p));
     p.x = x; p.h = codes; p.h_scale = scales;
@@ -1037,6 +1048,10 @@ extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, con
     if (!aligned16(a) || !aligned16(w) || !aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, pw) ||
         !aligned_to(gate, pw) || !aligned_to(residual, ow) || !aligned_to(out, ow) || !aligned_to(index, 4))
         return SBA_ERR_ALIGNMENT;
+    if (out == static_cast<const void*>(a) || out == static_cast<const void*>(w)) return SBA_ERR_INVALID_ARG;
+    if (out == residual && (heads > 0 || !in_place(residual, strides, out, strides + 2, B, 1, true) ||
+                            (N > 1 && strides[1] != strides[4])))
+        return SBA_ERR_INVALID_ARG;
     sba::LinearParams p;
     std::memset(&p, 0, sizeof(p));
     p.a_scale = a_scale; p.w_scale = w_scale; p.bias = bias; p.gate = gate; p.residual = residual;
@@ -1122,6 +1137,8 @@ extern "C" sba_status sba_rotary(const void* x, void* out, int dtype, const int3
         if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1e9 || axis[i] >= axes) return SBA_ERR_INVALID_ARG;
     const int w = dtype_bytes(dtype);
     if (!aligned_to(x, w) || !aligned_to(out, w) || !aligned_to(pos, 4)) return SBA_ERR_ALIGNMENT;
+    if (!in_place(x, strides, out, strides + 3, B, H, true) || (out == x && N > 1 && strides[2] != strides[5]))
+        return SBA_ERR_INVALID_ARG;
     sba::RotaryParams p;
     std::memset(&p, 0, sizeof(p));
     p.x = x; p.out = out; p.pos = pos;

@@ -497,6 +497,12 @@ def _elsewhere(device, stream):
     return torch.cuda.stream(stream)
 
 
+def _counts(*sizes):
+    """Refuse sizes that do not fit the C calls' 32-bit arguments (ctypes would cut them)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes {sizes}: each must be below 2^31")
+
+
 def _values(t, name, shape, device, dtype):
     """Check an optional tensor: shape, device, type, contiguous."""
     if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device):
@@ -630,6 +636,7 @@ def residual_norm(x, y=None, gate=None, norm="layer", weight=None, bias=None, sc
     if out_scale is not None and not quantize:
         raise ValueError("out_scale without quantize")
     if B and N:
+        _counts(B, N, C)
         _check(lib().sba_residual_norm(
             x.data_ptr(), _raw(y), _raw(x_out), _raw(out), _raw(out_scale), _DTYPES[xtype], _DTYPES[dtype], B, N, C,
             _Strides8(*strides), _raw(valid_len), _NORMS[norm], _raw(weight), _raw(bias), _NORMS[post_norm],
@@ -674,6 +681,7 @@ def token_quantize(x, codes=None, scales=None, stream=None):
     else:
         _values(scales, "scales", lead, dev, torch.float32)
     if B and N:
+        _counts(B, H, N, D)
         _check(lib().sba_token_quantize(x.data_ptr(), kind, B, H, N, D, _Strides3(sb, sh, sn), codes.data_ptr(),
                                         scales.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)), "sba_token_quantize")
     return codes, scales
@@ -736,6 +744,7 @@ def int8_linear(codes, scales, weight_codes, weight_scales, bias=None, activatio
     strides = out.stride()
     ob, oh, on = strides[:3] if heads else (strides[0], 0, strides[1]) if len(lead) == 2 else (0, 0, strides[0])
     if B and N:
+        _counts(B, N, K, M)
         _check(lib().sba_int8_linear(
             codes.data_ptr(), scales.data_ptr(), weight_codes.data_ptr(), weight_scales.data_ptr(), B, N, K, M,
             _raw(bias), _raw(gate), 2 if ptype is None else _DTYPES[ptype], G, _raw(index), _ACTS[activation],
@@ -831,6 +840,7 @@ def rotary(x, pos, table: RopeTable, layout: str = "interleaved", inverse: bool 
         if out.data_ptr() == x.data_ptr() and out.stride() != strides:
             raise ValueError("out at x's place with other strides")
     if B and H and N:
+        _counts(B, H, N, D)
         _check(lib().sba_rotary(x.data_ptr(), out.data_ptr(), dtype, pos.data_ptr(), table.axes, B, H, N, D,
                                 _Strides6(*strides[:3], *out.stride()[:3]), table.rope_dim, _LAYOUTS[layout],
                                 table._freq_at, table._axis_at, table.amplitude, int(inverse),
