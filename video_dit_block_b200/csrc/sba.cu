@@ -856,8 +856,12 @@ sba_status run_rows(const sba::RowParams& p, bool vec, cudaStream_t s) {
     const int chunks = p.quant ? p.Cq / 8 : (p.C + 7) / 8;
     if (!vec) {
         // the row may start up to 7 channels into its first chunk, and its codes are read back
-        // up to 4 bytes past their end
+        // up to 4 bytes past their end.  No more chunks a thread than needed: each one's ends
+        // cost (200,000 rows of 250 channels, gated residual and modulated norm: two chunks a
+        // thread 336, four 607 us)
         const int most = chunks + 2;
+        if (most <= 32) return launch_rows<XT, HT, true, 1, false, sba::kRowAny>(p, most, s);
+        if (most <= 64) return launch_rows<XT, HT, true, 2, false, sba::kRowAny>(p, most, s);
         if (most <= 128) return launch_rows<XT, HT, true, 4, false, sba::kRowAny>(p, most, s);
         if constexpr (XT == HT)
             if (row_kind(p) == sba::kRowQuant && most <= 4096)
