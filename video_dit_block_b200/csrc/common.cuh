@@ -8,8 +8,8 @@ namespace sba {
 
 enum DeviceError : int { kErrNone = 0, kErrTimeout = 5, kErrBadRouting = 6 };
 
-// One error word per device (the whole library is one translation unit).  The
-// first error recorded wins; sba_get_device_status reads and clears it.
+// One error word per device, in sba.cu's unit (the row operators, compiled apart, are given its
+// address).  The first error recorded wins; sba_get_device_status reads and clears it.
 __device__ int g_device_error;
 
 __device__ __forceinline__ void raise_device_error(int code) {

@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "../../include/sba.h"
 #include "common.cuh"
 
 namespace sba {
@@ -57,7 +58,12 @@ struct RowParams {
     int norm, post, quant;
     int param32;               // parameters are fp32 (else the 16-bit type)
     float eps;
+    int* error;                // the device's error word (with index)
 };
+
+// The launch for types XT, HT (as RowType); vec: rows and parameters on their wide grids.
+template <int XT, int HT>
+sba_status run_rows(const RowParams& p, bool vec, cudaStream_t s);
 
 // Two 16-bit values of a 32-bit word as floats, and back (one rounding, to nearest even).
 __device__ __forceinline__ void unpack16(uint32_t w, int fp16, float& a, float& b) {
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
         if (p.index) {
             g = p.index[at.row];
             if (g < 0 || g >= p.G) {
-                if (t == 0) raise_device_error(kErrBadRouting);
+                if (t == 0) atomicCAS(p.error, 0, (int)kErrBadRouting);
                 g = 0;
             }
         }

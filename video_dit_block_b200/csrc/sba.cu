@@ -1,6 +1,7 @@
 // sba.cu -- host side of the C ABI declared in include/sba.h: argument checks,
-// TMA tensor-map encoding, launches and the device status word.  The whole
-// library is this one translation unit (kernels come from the .cuh files).
+// TMA tensor-map encoding, launches and the device status word.  The kernels come from the
+// .cuh files; those of the row operators, many and long to compile, are in units of their
+// own (rows.cu).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -809,84 +810,12 @@ bool in_place(const void* in, const int64_t* si, const void* out, const int64_t*
     return in != out || (same_type && (B == 1 || si[0] == so[0]) && (N == 1 || si[1] == so[1]));
 }
 
-template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32 = true>
-sba_status launch_rows(const sba::RowParams& p, int chunks, cudaStream_t s) {
-    const auto kernel = sba::residual_norm_kernel<XT, HT, WARP, VPT, VEC, KIND, P32>;
-    const int threads = WARP ? 128 : (chunks + 32 * VPT - 1) / (32 * VPT) * 32;
-    const long long ctas = WARP ? (p.rows + 3) / 4 : p.rows;
-    long long grid = ctas;
-    const size_t smem = VEC || !p.quant ? 0 : (size_t)threads * VPT * 8;  // the codes of the CTA's rows
-    if (ctas > 128) {
-        int dev = 0, sms = 0, resident = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem) != cudaSuccess || resident < 1)
-            return SBA_ERR_CUDA;
-        if (ctas > (long long)sms * resident) grid = (long long)sms * resident;
-    }
-    kernel<<<(unsigned)grid, threads, smem, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
-}
-
-// Which of the kernels with fixed steps a call is.
-int row_kind(const sba::RowParams& p) {
-    if (!p.norm) return p.y ? sba::kRowAny : p.D ? sba::kRowQuantHeads : sba::kRowQuant;
-    const bool modulated = p.scale && p.shift && !p.bias;
-    if (!p.y && modulated) return p.quant ? sba::kRowNormQuant : sba::kRowNorm;
-    if (p.y && p.gate && !p.post && modulated) return p.quant ? sba::kRowGateNormQuant : sba::kRowGateNorm;
-    if (p.y && p.gate && p.post && !p.scale && !p.shift && !p.quant) return sba::kRowPostGateNorm;
-    return sba::kRowAny;
-}
-
-template <int XT, int HT, bool P32>
-sba_status run_kind(const sba::RowParams& p, int chunks, cudaStream_t s) {
-    switch (row_kind(p)) {
-        case sba::kRowNorm: return launch_rows<XT, HT, false, 4, true, sba::kRowNorm, P32>(p, chunks, s);
-        case sba::kRowNormQuant: return launch_rows<XT, HT, false, 4, true, sba::kRowNormQuant, P32>(p, chunks, s);
-        case sba::kRowGateNorm: return launch_rows<XT, HT, false, 4, true, sba::kRowGateNorm, P32>(p, chunks, s);
-        case sba::kRowGateNormQuant: return launch_rows<XT, HT, false, 4, true, sba::kRowGateNormQuant, P32>(p, chunks, s);
-        case sba::kRowPostGateNorm: return launch_rows<XT, HT, false, 4, true, sba::kRowPostGateNorm, P32>(p, chunks, s);
-    }
-    return launch_rows<XT, HT, false, 4, true, sba::kRowAny>(p, chunks, s);
-}
-
-// The warps of a row and the chunks of each thread.
-template <int XT, int HT>
-sba_status run_rows(const sba::RowParams& p, bool vec, cudaStream_t s) {
-    const int chunks = p.quant ? p.Cq / 8 : (p.C + 7) / 8;
-    if (!vec) {
-        // the row may start up to 7 channels into its first chunk, and its codes are read back
-        // up to 4 bytes past their end.  No more chunks a thread than needed: each one's ends
-        // cost (200,000 rows of 250 channels, gated residual and modulated norm: two chunks a
-        // thread 336, four 607 us)
-        const int most = chunks + 2;
-        if (most <= 32) return launch_rows<XT, HT, true, 1, false, sba::kRowAny>(p, most, s);
-        if (most <= 64) return launch_rows<XT, HT, true, 2, false, sba::kRowAny>(p, most, s);
-        if (most <= 128) return launch_rows<XT, HT, true, 4, false, sba::kRowAny>(p, most, s);
-        if constexpr (XT == HT)
-            if (row_kind(p) == sba::kRowQuant && most <= 4096)
-                return launch_rows<XT, HT, false, 4, false, sba::kRowQuant>(p, most, s);
-        if (most <= 1024) return launch_rows<XT, HT, false, 4, false, sba::kRowAny>(p, most, s);
-        return launch_rows<XT, HT, false, 9, false, sba::kRowAny>(p, most, s);
-    }
-    if (chunks <= 32) return launch_rows<XT, HT, true, 1, true, sba::kRowAny>(p, chunks, s);
-    if (chunks <= 128) return launch_rows<XT, HT, true, 4, true, sba::kRowAny>(p, chunks, s);
-    if constexpr (XT == HT) {
-        if (row_kind(p) == sba::kRowQuant) return launch_rows<XT, HT, false, 4, true, sba::kRowQuant>(p, chunks, s);
-        if (row_kind(p) == sba::kRowQuantHeads)
-            return launch_rows<XT, HT, false, 4, true, sba::kRowQuantHeads>(p, chunks, s);
-    }
-    if (chunks > 1024) return launch_rows<XT, HT, false, 8, true, sba::kRowAny>(p, chunks, s);
-    if constexpr (HT != sba::kRowFp32) return p.param32 ? run_kind<XT, HT, true>(p, chunks, s) : run_kind<XT, HT, false>(p, chunks, s);
-    return launch_rows<XT, HT, false, 4, true, sba::kRowAny>(p, chunks, s);
-}
-
 sba_status dispatch_rows(const sba::RowParams& p, int x_dtype, int dtype, bool vec, cudaStream_t s) {
-    if (x_dtype == SBA_DTYPE_BF16) return run_rows<0, 0>(p, vec, s);
-    if (x_dtype == SBA_DTYPE_FP16) return run_rows<1, 1>(p, vec, s);
-    if (dtype == SBA_DTYPE_BF16) return run_rows<2, 0>(p, vec, s);
-    if (dtype == SBA_DTYPE_FP16) return run_rows<2, 1>(p, vec, s);
-    return run_rows<2, 2>(p, vec, s);
+    if (x_dtype == SBA_DTYPE_BF16) return sba::run_rows<0, 0>(p, vec, s);
+    if (x_dtype == SBA_DTYPE_FP16) return sba::run_rows<1, 1>(p, vec, s);
+    if (dtype == SBA_DTYPE_BF16) return sba::run_rows<2, 0>(p, vec, s);
+    if (dtype == SBA_DTYPE_FP16) return sba::run_rows<2, 1>(p, vec, s);
+    return sba::run_rows<2, 2>(p, vec, s);
 }
 
 // Row-major [rows][K] 8-bit codes as a 2-D tensor; box = 128 codes x box_rows, 128-byte swizzle.
@@ -985,6 +914,8 @@ extern "C" sba_status sba_residual_norm(const void* x, const void* y, void* x_ou
     p.x = x; p.y = y; p.r = x_out; p.h = out; p.h_scale = out_scale;
     p.valid_len = valid_len;
     p.index = modulated ? index : nullptr;
+    if (p.index && cudaGetSymbolAddress(reinterpret_cast<void**>(&p.error), sba::g_device_error) != cudaSuccess)
+        return SBA_ERR_CUDA;
     p.gate = gate; p.scale = scale; p.shift = shift;
     p.weight = weight; p.bias = bias; p.post_weight = post_weight;
     p.x_sb = strides[0]; p.x_sn = strides[1]; p.y_sb = strides[2]; p.y_sn = strides[3];
