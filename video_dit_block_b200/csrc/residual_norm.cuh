@@ -407,8 +407,8 @@ __device__ __forceinline__ void row_step(uint64_t (&f)[VPT][4], const uint64_t (
 
 // The calls a transformer block makes have kernels of their own: in the general one
 // (kRowAny), which asks for every step as it goes, instruction fetch and issue cost more
-// than memory does (5120 channels in bf16, of the copy rate: the modulated norm 58%, with the
-// gated residual 80%; on their own 78% and 94%).
+// than memory does (37800 rows of 5120 channels in bf16, of the copy rate: the modulated norm
+// 58%, with the gated residual 80%; on their own 80% and 90 to 99%, 140 to 151 and 239 to 262 us).
 enum RowKind : int {
     kRowAny,
     kRowQuant,         // codes of plain rows
