@@ -689,6 +689,75 @@ def test_captured_and_replayed(sba):
             assert all(torch.equal(p, q) for p, q in zip(u, v))
 
 
+def test_calls_from_two_threads(sba):
+    """Products of other sizes, and the other calls, at once from two host threads."""
+    import threading
+    g = gen(42)
+    sizes = [(2, 64, 512), (40, 2048, 1024), (700, 4096, 256), (5, 320, 8192)]
+    ins = [linear_inputs(g, 1, n, k, m) for n, m, k in sizes]
+    more = calls(sba, g)
+    want = [sba.int8_linear(*i) for i in ins], [f() for f in more]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(which):
+        try:
+            s = torch.cuda.Stream()
+            for i in range(100):
+                j = (i + which) % len(ins)
+                got = sba.int8_linear(*ins[j], stream=s)
+                rest = more[i % len(more)](s)
+                s.synchronize()
+                if not torch.equal(got, want[0][j]) or not all(map(torch.equal, rest, want[1][i % len(more)])):
+                    wrong.append((which, i))
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(w,)) for w in (0, 1)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+
+
+@pytest.mark.parametrize("C", [256, 251])
+@pytest.mark.parametrize("far", ["samples", "tokens"])
+def test_offsets_past_32_bits(sba, C, far):
+    """Rows 2^31 elements apart."""
+    g = gen(43)
+    big = torch.empty((1 << 31) + (1 << 20), dtype=BF, device=DEV)
+    shape = (2, 3, C) if far == "samples" else (1, 2, C)
+    strides = (1 << 31, 2 * C + 5 if C % 8 else 2 * C, 1) if far == "samples" else (1 << 31, 1 << 31, 1)
+    place = lambda at: big.as_strided(shape, strides, at)
+    x, y, out = place(0), place(C + (8 - C % 8) % 8), place(1 << 16)
+    xs, ys = randn(g, *shape, dtype=BF), randn(g, *shape, dtype=BF)
+    x.copy_(xs)
+    y.copy_(ys)
+    gate = randn(g, shape[0], C)
+    r0, h0 = sba.residual_norm(xs, ys, gate=gate)
+    r, h = sba.residual_norm(x, y, gate=gate, out=out)
+    assert h.data_ptr() == out.data_ptr() and torch.equal(r, r0)  # (no sums in r)
+    # rows that start elsewhere on the 16-byte grid are summed in another order: two results within
+    # 400 u S and a rounding each of the same value
+    size = xs.double().abs() + ys.double().abs() * gate.double()[:, None].abs()
+    S = size.amax(-1, keepdim=True) / (xs.double() + ys.double() * gate.double()[:, None]).std(-1, keepdim=True, correction=0)
+    assert ((h.double() - h0.double()).abs() <= 800 * U * S + 2 * rounding(h0.double().abs() + 800 * U * S, BF)).all()
+    r, h = sba.residual_norm(xs, ys, gate=gate, x_out=out)
+    assert torch.equal(out, r0)
+    assert all(map(torch.equal, sba.token_quantize(x), sba.token_quantize(xs)))
+    a, s = sba.token_quantize(xs)
+    w, ws = sba.token_quantize(randn(g, C, 96 if C % 8 else 128))
+    a = a[..., :1].expand(*shape[:2], w.shape[1]).contiguous()
+    res = sba.int8_linear(a, s, w, ws, residual=xs)
+    assert torch.equal(sba.int8_linear(a, s, w, ws, residual=x, out=out), res)
+    table = sba.rope_frequencies(64 if C % 8 == 0 else 62)
+    pos = torch.arange(shape[1], device=DEV, dtype=torch.int32).expand(shape[:2]).contiguous()
+    want = sba.rotary(xs[:, None], pos, table)
+    got = sba.rotary(x[:, None], pos, table, out=out[:, None])
+    assert torch.equal(got, want)
+
+
 def test_empty_batches(sba):
     x = torch.empty(2, 0, 64, dtype=BF, device=DEV)
     r, h = sba.residual_norm(x, x)
