@@ -408,7 +408,7 @@ __device__ __forceinline__ void row_step(uint64_t (&f)[VPT][4], const uint64_t (
 // The calls a transformer block makes have kernels of their own: in the general one
 // (kRowAny), which asks for every step as it goes, instruction fetch and issue cost more
 // than memory does (37800 rows of 5120 channels in bf16, of the copy rate: the modulated norm
-// 58%, with the gated residual 80%; on their own 80% and 90 to 99%, 140 to 151 and 239 to 262 us).
+// 58%, with the gated residual 80%; on their own 83% and 91%, 144 and 259 us).
 enum RowKind : int {
     kRowAny,
     kRowQuant,         // codes of plain rows
@@ -420,6 +420,16 @@ enum RowKind : int {
     kRowPostGateNorm,  // post norm, gated residual, norm without them
 };
 
+// The CTAs an SM that a kernel's registers leave room for.  16-bit rows without a y need few, and
+// run faster at 80 registers (37800 x 5120: norm and modulation 144 us, with codes 155) than
+// at 128 (149 and 176); fp32 rows and rows with a y would spill.
+template <int XT, bool WARP, int VPT, int KIND>
+constexpr int row_ctas() {
+    if (WARP) return 4;
+    if (VPT > 4 || KIND == kRowQuant || KIND == kRowQuantHeads) return 1;
+    return XT != kRowFp32 && (KIND == kRowNorm || KIND == kRowNormQuant) ? 3 : 2;
+}
+
 // XT, HT: the types of x and r, and of y and h (as RowType).  WARP: four rows per CTA of four
 // warps; otherwise a row per CTA, and as many CTAs as are resident.  P32: parameters in fp32.
 template <int XT, int HT, bool WARP, int VPT, bool VEC, int KIND, bool P32>
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(WARP                  ? 128
                                   : KIND == kRowQuant || KIND == kRowQuantHeads ? 1024
                                   : VPT > 4                                     ? 512
                                                                                 : 256,
-                                  WARP ? 4 : VPT > 4 || KIND == kRowQuant || KIND == kRowQuantHeads ? 1 : 2) residual_norm_kernel(
+                                  (row_ctas<XT, WARP, VPT, KIND>())) residual_norm_kernel(
     const __grid_constant__ RowParams p) {
     __shared__ __align__(16) float red[2][32];
     extern __shared__ __align__(16) unsigned char code_rows[];  // without VEC: a row's codes
