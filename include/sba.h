@@ -423,7 +423,8 @@ sba_status sba_token_quantize(const void* x, int dtype, int B, int H, int N, int
  *   a, a_scale   int8 [B, N, K] and fp32 [B, N] contiguous, as sba_token_quantize or
  *                sba_residual_norm write them;  w, w_scale: int8 [M, K] and fp32 [M]
  *                (sba_token_quantize of the weight's rows).  K a multiple of 16, at most
- *                SBA_MAX_INT8_K (else SBA_ERR_UNSUPPORTED)
+ *                SBA_MAX_INT8_K; B * N at most 2^31 - 256, M at most 2^24 (else
+ *                SBA_ERR_UNSUPPORTED)
  *   bias         [M] or NULL;  gate [G, M] contiguous or NULL; of param_dtype, fp32 or
  *                out_dtype;  index int32 [B, N] contiguous, or NULL (then G >= B)
  *   activation   SBA_ACT_*;  the tanh form of GELU

@@ -861,6 +861,8 @@ LinearPlan plan_linear(long long M, long long N, long long K, int sms) {
             best = LinearPlan{bn, 0};
         }
     }
+    // the split kernel's row tiles are a grid's second dimension; the pair kernel takes more
+    if ((M + 127) / 128 > 65535) return best;
     const double box = M < 128 ? (double)((M + 7) / 8 * 8) : 128.0;
     for (int bn = 64; bn <= 128; bn += 64) {
         for (int splits = 1; splits <= 8 && (splits == 1 || ks >= 2 * splits); splits *= 2) {
@@ -1030,8 +1032,7 @@ extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, con
     using SM = sba::SplitSmem;
     p.box_rows = p.M < 128 ? (p.M + 7) / 8 * 8 : 128;
     const int splits = plan.splits;
-    const long long tiles_m = (p.M + 127ll) / 128, ctas = tiles_n * tiles_m * splits;
-    if (tiles_m > 65535 || tiles_n * splits > 0x7fffffffll) return SBA_ERR_UNSUPPORTED;
+    const long long tiles_m = (p.M + 127ll) / 128, ctas = tiles_n * tiles_m * splits;  // tiles_n * splits < 2^22
     // CTAs share an SM's memory, up to three where there are that many
     const int per_sm = ctas > 2 * sms ? 3 : ctas > sms ? 2 : 1;
     p.stages = sba::kMaxStages;
