@@ -450,8 +450,8 @@ sba_status sba_int8_linear(const int8_t* a, const float* a_scale, const int8_t* 
  *                out may be x (same strides)
  *   pos          int32 [B, N, axes] device contiguous
  *   rope_dim     even, in [2, min(D, 256)]
- *   inv_freq, axis  host arrays of rope_dim / 2: radians a position, and the position's
- *                axis, of each pair */
+ *   inv_freq, axis  host arrays of rope_dim / 2: radians a position (magnitude at most
+ *                1e9), and the position's axis, of each pair */
 sba_status sba_rotary(const void* x, void* out, int dtype, const int32_t* pos, int axes, int B, int H, int N, int D,
                       const int64_t* strides, int rope_dim, int layout, const double* inv_freq, const uint8_t* axis,
                       float amplitude, int inverse, void* stream);

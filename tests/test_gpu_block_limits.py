@@ -1,9 +1,11 @@
 """The block's operators at the ends of the ranges they document: products of more row tiles
-than a grid's second dimension holds."""
+than a grid's second dimension holds, and rotary frequencies of many turns a position."""
+from fractions import Fraction
+
 import pytest
 import torch
 
-from test_gpu_block import BF, DEV, clean_status, close, gen, linear_ref, randn, sba  # noqa: F401 (fixtures)
+from test_gpu_block import BF, DEV, SF, U, clean_status, close, gen, linear_ref, randn, sba  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +28,29 @@ def test_int8_linear_of_millions_of_rows(sba, B, N):
     heads = sba.int8_linear(a, sa, w, sw, bias=bias, heads=2)
     for h in range(2):
         assert torch.equal(heads[:, h], out[..., 32 * h:32 * h + 32])
+
+
+# 2 pi to 60 digits
+TWO_PI = Fraction(62831853071795864769252867665590057683943387987502116419499, 10 ** 58)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_rotary_of_many_turns_a_position(sba, layout):
+    """Frequencies up to the largest accepted, at positions up to the largest: the angle, taken modulo
+    a turn in exact arithmetic, is as exact as any (the bound of test_gpu_block.py)."""
+    g = gen(61)
+    freq = [1e9, -1e9, 999_999_937.0, 123_456_789.123, 1e6 / 3, 6.283185307179586, 1e3, 1.0,
+            0.1, 1e-3, 2.0 ** -20, 1e-9, 2.0 ** 29, 3.0 ** 18, -12_345.678, 1e-300]
+    pos = [0, 1, -1, 2, 1000, 65537, 2 ** 31 - 1, -2 ** 31, 1_234_567_890, -987_654_321]
+    table = sba.RopeTable(freq)
+    turns = [[Fraction(p) * Fraction(f) / TWO_PI for f in freq] for p in pos]
+    th = torch.tensor([[2 * torch.pi * float(t - round(t)) for t in row] for row in turns], dtype=torch.float64, device=DEV)
+    c, s = th.cos(), th.sin()
+    x = randn(g, 1, 3, len(pos), 48)  # 16 channels are copied
+    r = sba.rotary(x, torch.tensor(pos, dtype=torch.int32, device=DEV)[None], table, layout=layout)
+    one, two = (slice(0, 16), slice(16, 32)) if layout == "half" else (slice(0, 32, 2), slice(1, 32, 2))
+    ref, tol = x.double().clone(), torch.zeros_like(x, dtype=torch.float64)
+    u, v = x.double()[..., one], x.double()[..., two]
+    ref[..., one], ref[..., two] = u * c - v * s, u * s + v * c
+    tol[..., one] = tol[..., two] = 11 * U * (u.abs() + v.abs())
+    close(r, ref, tol, SF)

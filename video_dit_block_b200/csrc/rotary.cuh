@@ -11,8 +11,8 @@
 //
 // Angles.  A turn is 2^64: F_p = round(w_p / 2 pi * 2^64), formed on the host, and pos * F_p
 // modulo 2^64 drops whole turns exactly, so a position of 2^31 costs no more accuracy than
-// position 1 (2^-33 turns from the rounding of F_p, 2^-25 of the angle from its conversion
-// to fp32).
+// position 1, whatever the frequency (2^-34 turns from the rounding of F_p, 2^-25 of the
+// angle from its conversion to fp32).
 //
 // HBM-bound: x is read once and written once.  A thread owns 16 channels of one token in two
 // runs of 8, such that its neighbours' runs are next to its own, takes their sines and

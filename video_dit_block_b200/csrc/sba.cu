@@ -882,6 +882,28 @@ LinearPlan plan_linear(long long M, long long N, long long K, int sms) {
     return best;
 }
 
+// w radians, |w| <= 2^30, in turns, whole ones dropped: the nearest multiple of 2^-64, in 64 bits.  In
+// integers: a product in floating point has its 64 digits used up by the whole turns of a large w
+// (1e9 radians at position 2^31 were 0.09 radians off).
+uint64_t turn_fraction(double w) {
+    // 1 / (2 pi) * 2^192, lowest 64 bits first
+    constexpr uint64_t inv_two_pi[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+    int e;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(w), &e), 53);  // |w| = m * 2^(e - 53)
+    uint64_t product[5] = {};  // m / (2 pi) * 2^192: the turns are product * 2^(e - 245)
+    for (int i = 0; i < 3; ++i) {
+        const unsigned __int128 t = (unsigned __int128)m * inv_two_pi[i] + product[i];
+        product[i] = (uint64_t)t;
+        product[i + 1] = (uint64_t)(t >> 64);
+    }
+    const int drop = 181 - e;  // product's bits below 2^-64 of a turn: 151 at the least, since e <= 30
+    if (drop > 255) return 0;
+    const int i = drop / 64, b = drop % 64;
+    uint64_t f = product[i] >> b | (b ? product[i + 1] << (64 - b) : 0);
+    f += product[(drop - 1) / 64] >> ((drop - 1) % 64) & 1;
+    return w < 0 ? 0 - f : f;
+}
+
 }  // namespace
 
 extern "C" sba_status sba_residual_norm(const void* x, const void* y, void* x_out, void* out, float* out_scale,
@@ -1088,11 +1110,7 @@ extern "C" sba_status sba_rotary(const void* x, void* out, int dtype, const int3
     p.sin_amp = inverse ? -amplitude : amplitude;
     for (int i = 0; i < p.pairs; ++i) {
         p.axis[i] = axis[i];
-        // turns a position, whole ones dropped, in 64 fractional bits
-        long double t = (long double)inv_freq[i] * 0.159154943091895335768883763372514362L;
-        t -= std::floor(t);
-        const long double scaled = std::floor(t * 18446744073709551616.0L + 0.5L);
-        p.turn[i] = scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
+        p.turn[i] = turn_fraction(inv_freq[i]);
     }
     const bool vec = D % 16 == 0 && p.pairs % (p.half ? 8 : 4) == 0 && rows16(x, strides, 3, w) && rows16(out, strides + 3, 3, w);
     const long long per_token = vec ? D / 16 : (p.copy ? D - p.pairs : p.pairs);
