@@ -802,8 +802,10 @@ def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scalin
             raise ValueError("yarn scaling: base != 1, original_length >= 1 and 0 < beta_slow < beta_fast")
         # the pair index that turns `turns` times within the original length
         pair = lambda turns: d * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
-        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), d - 1)
-        ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(d // 2)]
+        slow = pair(beta_slow)
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(slow), d - 1)
+        # (no pair turns beta_slow times within a short length: then lo = hi = 0, and no ramp)
+        ramp = [1.0 if i >= slow else min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(d // 2)]
         freq = [f / factor * t + f * (1 - t) for f, t in zip(freq, ramp)]
         amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
     elif scaling not in (None, "ntk"):
