@@ -20,3 +20,11 @@ def test_yarn_scales_pairs_of_few_turns(rope, axes, length, slow):
         if turns >= 32 * (1 + 1e-12):
             assert f == pytest.approx(p, rel=1e-12), (turns, f / p)
         assert p / 4 * (1 - 1e-12) <= f <= p * (1 + 1e-12)
+
+
+@pytest.mark.parametrize("base", [0.5, 1.0, 1e-3])
+def test_yarn_refuses_a_base_of_at_most_one(base):
+    """Its frequencies do not fall with the pair, and the ramp runs over pairs of falling ones."""
+    import video_dit_block_b200 as sba
+    with pytest.raises(ValueError):
+        sba.rope_frequencies(64, base=base, scaling="yarn", factor=2.0)

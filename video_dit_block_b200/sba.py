@@ -798,8 +798,8 @@ def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scalin
     if scaling == "linear":
         freq = [f / factor for f in freq]
     elif scaling == "yarn":
-        if base == 1 or original_length < 1 or not 0 < beta_slow < beta_fast:
-            raise ValueError("yarn scaling: base != 1, original_length >= 1 and 0 < beta_slow < beta_fast")
+        if base <= 1 or original_length < 1 or not 0 < beta_slow < beta_fast:
+            raise ValueError("yarn scaling: base > 1, original_length >= 1 and 0 < beta_slow < beta_fast")
         # the pair index that turns `turns` times within the original length
         pair = lambda turns: d * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
         slow = pair(beta_slow)
