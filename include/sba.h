@@ -437,6 +437,11 @@ sba_status sba_int8_linear(const int8_t* a, const float* a_scale, const int8_t* 
                            const int32_t* index, int activation, const void* residual, void* out, int out_dtype,
                            int heads, const int64_t* strides, void* stream);
 
+/* How sba_int8_linear runs a product of `rows` = B * N on a GPU of `sms` SMs, by its sizes alone:
+ * *splits = 0, tiles of 256 x *columns, a CTA pair each; else tiles of 128 x *columns, a CTA each,
+ * with K in *splits parts whose sums a cluster adds.  Host only. */
+sba_status sba_int8_linear_plan(long long rows, int channels, int codes, int sms, int* columns, int* splits);
+
 #define SBA_ROPE_INTERLEAVED 0 /* pair p = channels (2p, 2p + 1) */
 #define SBA_ROPE_HALF 1        /* pair p = channels (p, p + rope_dim / 2) */
 

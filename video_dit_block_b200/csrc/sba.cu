@@ -989,6 +989,14 @@ extern "C" sba_status sba_token_quantize(const void* x, int dtype, int B, int H,
     return dispatch_rows(p, dtype, dtype, vec, static_cast<cudaStream_t>(stream));
 }
 
+extern "C" sba_status sba_int8_linear_plan(long long rows, int channels, int codes, int sms, int* columns, int* splits) {
+    if (rows <= 0 || channels <= 0 || codes <= 0 || sms <= 1 || !columns || !splits) return SBA_ERR_INVALID_ARG;
+    const LinearPlan plan = plan_linear(rows, channels, codes, sms);
+    *columns = plan.bn;
+    *splits = plan.splits;
+    return SBA_OK;
+}
+
 extern "C" sba_status sba_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
                                       int B, int N, int K, int M, const void* bias, const void* gate, int param_dtype,
                                       int G, const int32_t* index, int activation, const void* residual, void* out,

@@ -108,6 +108,8 @@ def lib() -> ctypes.CDLL:
         L.sba_int8_linear.restype = i32
         L.sba_int8_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i32, vp, i32, vp, vp, i32, i32, vp,
                                       vp]
+        L.sba_int8_linear_plan.restype = i32
+        L.sba_int8_linear_plan.argtypes = [ctypes.c_longlong, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
         L.sba_rotary.restype = i32
         L.sba_rotary.argtypes = [vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, i32, i32, vp, vp, f32, i32, vp]
         L.sba_strerror.restype = ctypes.c_char_p
