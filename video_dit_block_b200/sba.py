@@ -774,6 +774,10 @@ class RopeTable:
         self._axis = (ctypes.c_uint8 * n)(*self.axis)
         self._freq_at, self._axis_at = ctypes.addressof(self._freq), ctypes.addressof(self._axis)
 
+    def __reduce__(self):
+        # a copy makes its own arrays: the addresses are of this table's
+        return RopeTable, (self.inv_freq, self.axis, self.amplitude)
+
 
 def rope_frequencies(rope_dim: int, axes: int = 1, base: float = 10000.0, scaling=None, factor: float = 1.0,
                      original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0) -> RopeTable:
