@@ -350,10 +350,12 @@ sba_status sba_gather_tokens(const void* src, int B, int H, int N, int row_bytes
  * strides whose last dimension is contiguous; strides are in elements, not negative, and
  * 0 only where an input is broadcast.  Pointers need the alignment of their element only
  * (16 bytes for int8 codes); rows whose addresses are all multiples of 16 bytes run
- * faster.  An output may be the input of the same shape, type and strides named below as
+ * faster.  B * N is below 2^31 (limits past that stand with each call: SBA_ERR_UNSUPPORTED).
+ * An output may be the input of the same shape, type and strides named below as
  * allowed (at an input's address otherwise: SBA_ERR_INVALID_ARG); outputs overlap
- * nothing else.  Statistics, sums and products are in fp32 (the integer sums exact) and
- * each output is rounded once, to nearest even.  An index outside its table raises
+ * nothing else.  Statistics, sums and products are in fp32 (the integer sums exact; a row's
+ * squares have to fit too, so magnitudes to 1e17) and each output is rounded once, to
+ * nearest even.  An index outside its table raises
  * SBA_ERR_DEVICE_FLAG and reads row 0. */
 typedef enum { SBA_DTYPE_BF16 = 0, SBA_DTYPE_FP16 = 1, SBA_DTYPE_FP32 = 2 } sba_dtype;
 
@@ -361,7 +363,7 @@ typedef enum { SBA_DTYPE_BF16 = 0, SBA_DTYPE_FP16 = 1, SBA_DTYPE_FP32 = 2 } sba_
 #define SBA_NORM_LAYER 1 /* (r - mean r) / sqrt(mean (r - mean r)^2 + eps) */
 #define SBA_NORM_RMS 2   /* r / sqrt(mean r^2 + eps) */
 
-/* Widest row of the calls below. */
+/* Widest row (C, or H * D) of sba_residual_norm and sba_token_quantize. */
 #define SBA_MAX_CHANNELS 32768
 
 /* The step between two sub-blocks of a transformer block, in one pass: the gated residual
@@ -452,8 +454,8 @@ sba_status sba_int8_linear_plan(long long rows, int channels, int codes, int sms
  * Angles are taken modulo a turn in 64-bit integers, so any int32 position is as exact as
  * a small one; fp32 arithmetic, one rounding.
  *   x, out       [B, H, N, D] of dtype at strides (sample, head, token) x, then out;
- *                out may be x (same strides)
- *   pos          int32 [B, N, axes] device contiguous
+ *                out may be x (same strides).  B and H at most 65535, D at most 2^20
+ *   pos          int32 [B, N, axes] device contiguous, axes at most 255
  *   rope_dim     even, in [2, min(D, 256)]
  *   inv_freq, axis  host arrays of rope_dim / 2: radians a position (magnitude at most
  *                1e9), and the position's axis, of each pair */

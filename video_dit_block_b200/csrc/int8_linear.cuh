@@ -15,13 +15,17 @@
 //                     its 128 rows of W, which halves the shared-memory traffic of W and
 //                     leaves it 64 bytes a clock of the 128.  Persistent: the accumulators of
 //                     two tiles alternate in TMEM, so the eight epilogue warps finish one
-//                     tile while the MMAs of the next run.  8192 x 5120 x 5120 codes: 134 us,
-//                     0.98 of twice the measured bf16 rate, with gate and residual 146.
+//                     tile while the MMAs of the next run.  8192 x 5120 x 5120 codes, random ones,
+//                     20 launches after a pause: 140 us, 0.94 of twice the measured bf16
+//                     rate, with gate and residual 153.  Without a pause the power cap
+//                     takes the clock to 1.3 GHz: 160 and 180.
 //   int8_split_kernel few rows or few tiles.  One CTA per tile of 128 x bn and K split; the
 //                     splits of a tile form a cluster and add their integer sums through
 //                     distributed shared memory (exact in any order).  With few rows it
-//                     streams W once: HBM-bound.  2 rows, 24576 x 4096 codes: 15.0 us, W's
-//                     bytes at the rate of a copy.
+//                     streams W once.  2 rows, 24576 x 4096 codes, weights in turn that
+//                     together exceed L2: 20.0 us, W's bytes (101 MB) at 0.77 of the copy
+//                     rate; the rest goes, as far as the code shows, to the CTAs' start.
+//                     (The same weight again and again is found in L2 in part: 14.7 us.)
 //
 // Every wait is bounded: on expiry the CTA records SBA_ERR_TIMEOUT, unwinds all roles,
 // drains its own loads and MMAs and frees its TMEM.

@@ -408,7 +408,7 @@ __device__ __forceinline__ void row_step(uint64_t (&f)[VPT][4], const uint64_t (
 // The calls a transformer block makes have kernels of their own: in the general one
 // (kRowAny), which asks for every step as it goes, instruction fetch and issue cost more
 // than memory does (37800 rows of 5120 channels in bf16, of the copy rate: the modulated norm
-// 58%, with the gated residual 80%; on their own 83% and 91%, 144 and 259 us).
+// 58%, with the gated residual 80%; on their own 81% and 94%, 146 and 252 us).
 enum RowKind : int {
     kRowAny,
     kRowQuant,         // codes of plain rows
@@ -421,8 +421,8 @@ enum RowKind : int {
 };
 
 // The CTAs an SM that a kernel's registers leave room for.  16-bit rows without a y need few, and
-// run faster at 80 registers (37800 x 5120: norm and modulation 144 us, with codes 155) than
-// at 128 (149 and 176); fp32 rows and rows with a y would spill.
+// run faster at 80 registers (37800 x 5120, side by side: norm and modulation 144 us, with codes
+// 155) than at 128 (149 and 176); fp32 rows and rows with a y would spill.
 template <int XT, bool WARP, int VPT, int KIND>
 constexpr int row_ctas() {
     if (WARP) return 4;

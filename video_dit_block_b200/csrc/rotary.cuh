@@ -17,8 +17,10 @@
 // HBM-bound: x is read once and written once.  A thread owns 16 channels of one token in two
 // runs of 8, such that its neighbours' runs are next to its own, takes their sines and
 // cosines once and applies them to all heads of its chunk, four heads' loads in flight at a
-// time (two of fp32).  Three CTAs an SM: with 40 heads of 128 bf16 channels, all turned, 119 us
-// for 37824 tokens, the rate of a copy; two CTAs (no register limit) take 133, four 134 us.
+// time (two of fp32).  Three CTAs an SM: with 40 heads of 128 bf16 channels, all turned, 119 to
+// 121 us for 37824 tokens, the rate of a copy; two CTAs (no register limit) take 133, four 134 us.
+// Widths off the vector form's multiples move value by value: 60 of 128 channels on three axes
+// take 402 us where 96 take 122.
 #pragma once
 #include <cstdint>
 

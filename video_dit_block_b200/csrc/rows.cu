@@ -31,7 +31,16 @@ static sba_status launch_rows(const RowParams& p, int chunks, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? SBA_OK : SBA_ERR_CUDA;
 }
 
-// Which of the kernels with fixed steps a call is.
+// Which of the kernels with fixed steps a call is.  The rule: the steps of a block whose norms are
+// modulated (scale and shift together, no bias), with the gated residual or without a y, and of one
+// with a norm after the block (then without modulation); all other combinations take the general
+// kernel.  What that leaves them at, 37800 rows of 5120 channels in bf16, as shares of the copy rate
+// (20 launches after a pause): with kernels of their own, modulated norm 146 us (0.81), gated residual
+// and modulated norm 252 (0.94), with codes 236 (0.88), fp32 stream with post norm, gate, RMS
+// norm and weight 390 (0.91); in the general one, ungated residual, RMS norm and weight 253 (0.93),
+// with the gate 273 (0.87), RMS norm and weight 170 (0.69), with codes 191 (0.46), layer norm, weight
+// and bias 202 (0.59), these and modulation 255 (0.46), post norm and modulation 340 (0.70), fp32 h
+// 304 (0.78).
 static int row_kind(const RowParams& p) {
     if (!p.norm) return p.y ? kRowAny : p.D ? kRowQuantHeads : kRowQuant;
     const bool modulated = p.scale && p.shift && !p.bias;
@@ -61,7 +70,7 @@ sba_status run_rows(const RowParams& p, bool vec, cudaStream_t s) {
         // the row may start up to 7 channels into its first chunk, and its codes are read back
         // up to 4 bytes past their end.  No more chunks a thread than needed: each one's ends
         // cost (200,000 rows of 250 channels, gated residual and modulated norm: two chunks a
-        // thread 336, four 607 us)
+        // thread 296 to 336, four 607 us)
         const int most = chunks + 2;
         if (most <= 32) return launch_rows<XT, HT, true, 1, false, kRowAny>(p, most, s);
         if (most <= 64) return launch_rows<XT, HT, true, 2, false, kRowAny>(p, most, s);
